@@ -128,6 +128,11 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   }
 }
 
+// Generic-proxy shared-memory writes -> visible to the async proxy (bulk copies, tensor cores).
+__device__ __forceinline__ void fence_proxy_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 // Order this thread's earlier generic-proxy global writes before later
 // async-proxy accesses (bulk copies) of the same memory.
 __device__ __forceinline__ void fence_proxy_async_global() {

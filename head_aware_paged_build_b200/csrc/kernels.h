@@ -151,4 +151,87 @@ struct BlockMassLaunch {
 };
 cudaError_t launch_block_mass(const BlockMassLaunch& a, cudaStream_t s);
 
+// Attention of a drafted tree over the pages and over the draft itself
+// (segpaged_tree_attention).  The work split is made on the device, from the
+// context lengths in the table (tree_common.cuh): the launch only says how a
+// kernel tiles its rows.
+struct TreeLaunch {
+  const HeadDesc* heads;
+  const PageDesc* pages;
+  int32_t n_heads, num_kv_heads, num_q_heads, group;
+  int32_t D, P;
+  bool bf16, fp8;
+  int64_t page_bytes, pool_pages;
+  const void* kpool;
+  const void* vpool;
+  const void* q;        // [B, T, Hq, D]
+  const void* k_draft;  // element (b, i, kv, x) at b*ds_seq + i*ds_tok + kv*ds_head + x
+  const void* v_draft;
+  int64_t ds_seq, ds_tok, ds_head;
+  const int32_t* parents;    // [B, T]
+  const int32_t* num_nodes;  // [B], or null: T each
+  int32_t T;
+  void* out;   // [B, T, Hq, D]
+  float* lse;  // [B, T, Hq] or null
+  float scale_log2;    // softmax scale * log2(e) (* k_scale for E4M3 pages)
+  float v_scale;       // E4M3 pages: value scale, applied to the normalised output
+  float k_inv, v_inv;  // E4M3 pages: 1 / k_scale, 1 / v_scale (the draft's rows are quantised as the append does)
+  int32_t nodes_per_group;  // nodes whose rows (nodes x group) one work item takes
+  int32_t n_ctas;
+  float* partial;     // workspace slots, two for each CTA
+  int32_t* counters;  // workspace arrival counters, kMaxTreeNodes for each head (zero between calls)
+  int32_t* status;
+};
+// How a kernel tiles a call: which kernel, its row group and its grid.
+struct TreeConfig {
+  bool tensor;  // the tcgen05 kernel (bf16 pages)
+  int32_t nodes_per_group;
+  int32_t rows_per_group;  // nodes_per_group * group
+  int32_t n_ctas;
+};
+TreeConfig tree_config(const sp_plan* plan, int32_t nodes);
+cudaError_t launch_tree(const TreeLaunch& a, const TreeConfig& c, cudaStream_t s);
+
+// Appending the accepted path of each sequence (segpaged_tree_commit).
+struct CommitLaunch {
+  HeadDesc* heads;  // device table, updated in place
+  PageDesc* pages;
+  int32_t n_heads;
+  int32_t D, P;
+  bool bf16, fp8;
+  float k_inv, v_inv;
+  int64_t ds_seq, ds_tok, ds_head, page_bytes, pool_pages;
+  const void* k_draft;
+  const void* v_draft;
+  const int32_t* path;      // [B, max_path] node indices
+  const int32_t* path_len;  // [B]
+  int32_t max_path, n_nodes;
+  void* kpool;
+  void* vpool;
+  int32_t* status;
+  int32_t* free_pool;
+};
+cudaError_t launch_commit(const CommitLaunch& a, cudaStream_t s);
+
+// Giving sequences other sequences' caches (segpaged_reorder).  Passed by
+// value (__grid_constant__), the sequences' layout classes and the kv-heads'
+// record ranges included.
+constexpr int kReorderMaxBatch = 2048;
+constexpr int kReorderMaxKvHeads = 1024;
+struct ReorderLaunch {
+  HeadDesc* heads;  // device table, updated in place
+  PageDesc* pages;
+  int32_t batch, num_kv_heads;
+  int64_t page_bytes, pool_pages;
+  const int32_t* parents;     // [B]
+  const int32_t* common_len;  // [B] or null
+  uint8_t* kpool;
+  uint8_t* vpool;
+  int32_t* status;
+  int32_t* free_pool;
+  int32_t rec_begin[kReorderMaxKvHeads + 1];  // CTA range of each kv-head: one CTA for each record index
+  uint16_t layout[kReorderMaxBatch];          // sequences may swap only within a layout class
+};
+cudaError_t launch_reorder(const ReorderLaunch& a, cudaStream_t s);
+
 }  // namespace sp

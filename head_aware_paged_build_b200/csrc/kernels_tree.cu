@@ -1,0 +1,564 @@
+// Attention of a drafted tree over the paged cache: the mma.sync kernel
+// (E4M3 pages, and small row counts on bf16 pages) and the fp32 kernel.
+//
+// mma.sync kernel: a producer warp streams the piece's pages into a ring of
+// shared-memory stages with bulk copies, as decode does, and writes the
+// draft's rows as one more page of the same layout (E4M3 pages: quantised as
+// an append would, so a node sees exactly the codes the cache will hold once
+// the node is committed).  WR x WT consumer warps: warp (wr, wt) holds rows
+// 16 wr .. 16 wr + 15 of the row group and takes 64 / WT of each page's
+// tokens, 16 at a time: S = Q K^T, online softmax with a lazy rescale, O += P V
+// on m16n8k16 fragments.  Scores, sums and O are fp32; P is rounded to the
+// type of the pages' operands (bf16, or f16 over widened E4M3 codes), V's own
+// type, while the sums use the unrounded weights.
+#include "tree_common.cuh"
+
+namespace sp {
+namespace {
+
+constexpr int kDraftPage = -2;  // phys of the draft's page in a stage's record
+constexpr float kLazyLog2 = 8.f;
+
+template <int D, bool FP8, int WR, int WT>
+struct TreeMma {
+  static constexpr int kConsumers = WR * WT;
+  static constexpr int kThreads = (kConsumers + 1) * 32;
+  static constexpr int kRows = 16 * WR;
+  static constexpr int kPageBytes = 64 * D * (FP8 ? 1 : 2);
+  static constexpr int kStages = (WR > 1 ? 128 : 64) * 1024 / (2 * kPageBytes) < 8
+                                     ? (WR > 1 ? 128 : 64) * 1024 / (2 * kPageBytes)
+                                     : 8;
+  static constexpr int kPitch = D + 8;
+  static constexpr int kMergeOff = kStages * 2 * kPageBytes;
+  static constexpr int kMlOff = kMergeOff + (WT - 1) * kRows * kPitch * 4;
+  static constexpr int kDescOff = kMlOff + (WT - 1) * kRows * 2 * 4;
+  static constexpr int kBarOff = kDescOff + kStages * 16;
+  static constexpr int kScanOff = kBarOff + 2 * kStages * 8;
+  static constexpr int kParOff = kScanOff + (kConsumers + 1 + 2) * 8;
+  static constexpr int kBytes = kParOff + kMaxTreeNodes * 2 + 16;
+  using Split = TreeSplit<1, 4, 8>;
+};
+
+template <int D, bool FP8, int WR, int WT>
+__global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 : 2) tree_mma_kernel(TreeLaunch a) {
+  using C = TreeMma<D, FP8, WR, WT>;
+  using Split = typename C::Split;
+  constexpr int P = 64, PB = C::kPageBytes, NST = C::kStages, NC = C::kConsumers;
+  constexpr int KSTEPS = D / 16, NT = D / 8, CHUNKS = 4 / WT;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ int s_last;
+  uint8_t* stage = smem;
+  float* mbuf = reinterpret_cast<float*>(smem + C::kMergeOff);
+  float* mlbuf = reinterpret_cast<float*>(smem + C::kMlOff);
+  PageDesc* sdesc = reinterpret_cast<PageDesc*>(smem + C::kDescOff);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  uint64_t* empty = full + NST;
+  int64_t* scratch = reinterpret_cast<int64_t*>(smem + C::kScanOff);
+  int16_t* par = reinterpret_cast<int16_t*>(smem + C::kParOff);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], NC);
+    }
+    fence_barrier_init();
+  }
+  Split split;
+  if (!split.template init<C::kThreads>(a, scratch)) return;  // its barriers order the mbarriers' init too
+  typename Split::Walk walk = split.walk();
+  typename Split::Piece pc;
+  int k = 0;  // pages streamed so far
+
+  if (warp == NC) {
+    // ------------------------------ producer ------------------------------
+    const uint8_t* kpool = static_cast<const uint8_t*>(a.kpool);
+    const uint8_t* vpool = static_cast<const uint8_t*>(a.vpool);
+    bool ok = true;
+    while (ok && split.next(a, walk, pc)) {
+      const PageDesc* rec = a.pages + pc.hd.vpage_begin;
+      int4 mine = make_int4(0, 0, 0, 0);
+      for (int p = pc.p0; ok && p < pc.p1; ++p, ++k) {
+        const int i = (p - pc.p0) & 31;
+        if (i == 0 && p + lane < pc.live) mine = *reinterpret_cast<const int4*>(rec + p + lane);
+        PageDesc pg;
+        pg.phys = __shfl_sync(0xffffffffu, mine.x, i);
+        pg.abs_start = __shfl_sync(0xffffffffu, mine.y, i);
+        pg.span = __shfl_sync(0xffffffffu, mine.z, i);
+        pg.head = pc.head;
+        const int s = k % NST;
+        ok = k < NST || __shfl_sync(0xffffffffu, int(lane == 0 && mbar_wait(&empty[s], ((k / NST) & 1) ^ 1)), 0);
+        if (!ok) {
+          if (lane == 0) record_error(a.status, kDevTimeoutEmpty);
+          break;
+        }
+        uint8_t* kd = stage + s * 2 * PB;
+        if (p >= pc.live) {  // the draft's page
+          for (int e = lane; e < 2 * PB / 16; e += 32) reinterpret_cast<uint4*>(kd)[e] = make_uint4(0, 0, 0, 0);
+          __syncwarp();
+          const int64_t base = int64_t(pc.hd.b) * a.ds_seq + int64_t(pc.hd.kv) * a.ds_head;
+          const __nv_bfloat16* kn = static_cast<const __nv_bfloat16*>(a.k_draft) + base;
+          const __nv_bfloat16* vn = static_cast<const __nv_bfloat16*>(a.v_draft) + base;
+          for (int t = 0; t < pc.n; ++t)
+            append_write_token<__nv_bfloat16, D, P, FP8>(kn + t * a.ds_tok, vn + t * a.ds_tok, kd, kd + PB, t,
+                                                         a.k_inv, a.v_inv, lane, 32);
+          fence_proxy_async_smem();  // before a later bulk copy into this stage
+          __syncwarp();
+          if (lane == 0) {
+            sdesc[s] = PageDesc{kDraftPage, 0, 0, pc.head};
+            mbar_arrive(&full[s]);
+          }
+        } else if (lane == 0) {
+          if (slot_hi(pg) > slot_lo(pg) && (pg.phys < 0 || pg.phys >= a.pool_pages)) {
+            record_error(a.status, kDevBadPage);  // corrupted table: report, read nothing
+            pg.span = 0;
+          }
+          sdesc[s] = pg;
+          if (slot_hi(pg) > slot_lo(pg)) {
+            mbar_arrive_expect_tx(&full[s], 2 * PB);
+            bulk_g2s(kd, kpool + int64_t(pg.phys) * a.page_bytes, PB, &full[s]);
+            bulk_g2s(kd + PB, vpool + int64_t(pg.phys) * a.page_bytes, PB, &full[s]);
+          } else {
+            mbar_arrive(&full[s]);  // an empty record: nothing to read
+          }
+        }
+      }
+    }
+    if (lane == 0)  // never leave with copies in flight
+      for (int j = (k > NST ? k - NST : 0); j < k; ++j)
+        if (!mbar_wait(&full[j % NST], (j / NST) & 1)) break;
+    return;
+  }
+
+  // ------------------------------ consumers ------------------------------
+  auto bar = [] { asm volatile("bar.sync 1, %0;" ::"n"(NC * 32) : "memory"); };
+  const int wr = warp / WT, wt = warp % WT;
+  const int grp = lane >> 2, tq = lane & 3, mi = lane >> 3, rr = lane & 7;
+  const int G = a.group;
+  const int row[2] = {wr * 16 + grp, wr * 16 + grp + 8};
+  bool ok = true;
+  while (split.next(a, walk, pc)) {
+    bar();  // every warp is done with the previous piece's parents and merge buffers
+    if (threadIdx.x < pc.n) par[threadIdx.x] = tree_parent(a, pc.hd.b, threadIdx.x);
+    bar();
+    const int rows = pc.nodes * G;
+    const int p_last = pc.hd.ctx_len + pc.n - 1;
+    int pos[2] = {0, 0};
+    uint64_t anc[2] = {0, 0};
+    uint32_t qa[KSTEPS][4];
+    const __nv_bfloat16* qrow[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      qrow[x] = nullptr;
+      if (row[x] < rows) {
+        int depth;
+        tree_node(par, pc.node0 + row[x] / G, pc.hd, depth, anc[x]);
+        pos[x] = pc.hd.ctx_len + depth;
+        qrow[x] = static_cast<const __nv_bfloat16*>(a.q) +
+                  ((int64_t(pc.hd.b) * a.T + pc.node0 + row[x] / G) * a.num_q_heads + pc.hd.kv * G + row[x] % G) * D;
+      }
+    }
+    if constexpr (FP8) {  // k-steps 2j, 2j+1 cover dims 32j .. 32j+31 in the K loads' order
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) {
+        const int c0 = j * 32 + tq * 8;
+        const uint4 x0 = qrow[0] ? *reinterpret_cast<const uint4*>(qrow[0] + c0) : make_uint4(0, 0, 0, 0);
+        const uint4 x1 = qrow[1] ? *reinterpret_cast<const uint4*>(qrow[1] + c0) : make_uint4(0, 0, 0, 0);
+        qa[2 * j][0] = bf16x2_to_f16x2(x0.x), qa[2 * j][2] = bf16x2_to_f16x2(x0.y);
+        qa[2 * j + 1][0] = bf16x2_to_f16x2(x0.z), qa[2 * j + 1][2] = bf16x2_to_f16x2(x0.w);
+        qa[2 * j][1] = bf16x2_to_f16x2(x1.x), qa[2 * j][3] = bf16x2_to_f16x2(x1.y);
+        qa[2 * j + 1][1] = bf16x2_to_f16x2(x1.z), qa[2 * j + 1][3] = bf16x2_to_f16x2(x1.w);
+      }
+    } else {
+#pragma unroll
+      for (int kk = 0; kk < KSTEPS; ++kk)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          qa[kk][x] = qrow[x] ? *reinterpret_cast<const uint32_t*>(qrow[x] + kk * 16 + tq * 2) : 0u;
+          qa[kk][x + 2] = qrow[x] ? *reinterpret_cast<const uint32_t*>(qrow[x] + kk * 16 + tq * 2 + 8) : 0u;
+        }
+    }
+    float o[NT][4];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+    for (int p = pc.p0; p < pc.p1; ++p, ++k) {
+      const int s = k % NST;
+      // the wait's outcome is voted: ldmatrix and mma.sync need the whole warp
+      if (ok && !__all_sync(0xffffffffu, mbar_wait(&full[s], (k / NST) & 1))) {
+        record_error(a.status, kDevTimeoutFull);
+        ok = false;
+      }
+      const PageDesc pg = sdesc[s];
+      const bool draft = pg.phys == kDraftPage;
+      const bool all = !draft && tree_page_full(pg, pc.hd, p_last);
+      uint64_t vis[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        vis[x] = row[x] >= rows ? 0 : all ? ~uint64_t(0) : draft ? anc[x] : tree_page_mask(pg, pc.hd, pos[x]);
+      const uint32_t kst = smem_u32(stage + s * 2 * PB), vst = kst + PB;
+      const uint8_t* kp8 = stage + s * 2 * PB;
+#pragma unroll
+      for (int c = 0; c < CHUNKS; ++c) {
+        const int tok0 = (wt * CHUNKS + c) * 16;
+        const uint32_t v0 = uint32_t(vis[0] >> tok0) & 0xffffu, v1 = uint32_t(vis[1] >> tok0) & 0xffffu;
+        if (!ok || !__any_sync(0xffffffffu, v0 | v1)) continue;
+        float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        if constexpr (FP8) {
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const uint2 u =
+                  *reinterpret_cast<const uint2*>(kp8 + fp8_kpage_offset(tok0 + n * 8 + grp, j * 32 + tq * 8, D));
+              mma_f16_16816(sc[n], qa[2 * j], e4m3x2_to_f16x2(uint16_t(u.x)), e4m3x2_to_f16x2(uint16_t(u.x >> 16)));
+              mma_f16_16816(sc[n], qa[2 * j + 1], e4m3x2_to_f16x2(uint16_t(u.y)),
+                            e4m3x2_to_f16x2(uint16_t(u.y >> 16)));
+            }
+        } else {
+          const int ktok = tok0 + (mi >> 1) * 8 + rr;
+#pragma unroll
+          for (int kk = 0; kk < KSTEPS; ++kk) {
+            uint32_t b0, b1, b2, b3;
+            ldmatrix_x4(b0, b1, b2, b3, kst + uint32_t(kpage_chunk_offset_bf16(ktok, 2 * kk + (mi & 1), P)));
+            mma_bf16_16816(sc[0], qa[kk], b0, b1);
+            mma_bf16_16816(sc[1], qa[kk], b2, b3);
+          }
+        }
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bool see = ((e < 2 ? v0 : v1) >> (n * 8 + tq * 2 + (e & 1))) & 1;
+            sc[n][e] = see ? sc[n][e] * a.scale_log2 : -INFINITY;
+            mx[e >> 1] = fmaxf(mx[e >> 1], sc[n][e]);
+          }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 1));
+          mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 2));
+        }
+        if (__any_sync(0xffffffffu, mx[0] > m[0] + kLazyLog2 || mx[1] > m[1] + kLazyLog2)) {
+          float al[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float mn = mx[x] > m[x] + kLazyLog2 ? mx[x] : m[x];
+            al[x] = mn == m[x] ? 1.f : fast_exp2(m[x] - mn);
+            l[x] *= al[x], m[x] = mn;
+          }
+#pragma unroll
+          for (int j = 0; j < NT; ++j) o[j][0] *= al[0], o[j][1] *= al[0], o[j][2] *= al[1], o[j][3] *= al[1];
+        }
+        const float b0 = m[0] == -INFINITY ? 0.f : m[0], b1 = m[1] == -INFINITY ? 0.f : m[1];
+        float pr[2][4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          pr[n][0] = fast_exp2(sc[n][0] - b0), pr[n][1] = fast_exp2(sc[n][1] - b0);
+          pr[n][2] = fast_exp2(sc[n][2] - b1), pr[n][3] = fast_exp2(sc[n][3] - b1);
+        }
+        l[0] += (pr[0][0] + pr[0][1]) + (pr[1][0] + pr[1][1]);
+        l[1] += (pr[0][2] + pr[0][3]) + (pr[1][2] + pr[1][3]);
+        uint32_t pa[4];
+        if constexpr (FP8) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+            pa[2 * n] = pack_f16x2(pr[n][0], pr[n][1]), pa[2 * n + 1] = pack_f16x2(pr[n][2], pr[n][3]);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            const uint32_t u =
+                *reinterpret_cast<const uint32_t*>(kp8 + PB + fp8_vpage_offset(j * 8 + grp, tok0 + tq * 4));
+            mma_f16_16816(o[j], pa, e4m3x2_to_f16x2(uint16_t(u)), e4m3x2_to_f16x2(uint16_t(u >> 16)));
+          }
+        } else {
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+            pa[2 * n] = pack_bf16x2(pr[n][0], pr[n][1]), pa[2 * n + 1] = pack_bf16x2(pr[n][2], pr[n][3]);
+          const int vc = (tok0 >> 3) + (mi & 1);
+#pragma unroll
+          for (int j = 0; j < NT / 2; ++j) {
+            const int dd = (2 * j + (mi >> 1)) * 8 + rr;
+            uint32_t b0, b1, b2, b3;
+            ldmatrix_x4(b0, b1, b2, b3, vst + uint32_t(vpage_chunk_offset_bf16(dd, vc)));
+            mma_bf16_16816(o[2 * j], pa, b0, b1);
+            mma_bf16_16816(o[2 * j + 1], pa, b2, b3);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[s]);
+    }
+
+    // ---- the row's WT warps join, in warp order ----
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+    }
+    if constexpr (WT > 1) {
+      if (wt > 0) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int at = (wt - 1) * C::kRows + row[x];
+          if (tq == 0) mlbuf[at * 2] = m[x], mlbuf[at * 2 + 1] = l[x];
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            *reinterpret_cast<float2*>(mbuf + at * C::kPitch + j * 8 + tq * 2) =
+                make_float2(o[j][2 * x], o[j][2 * x + 1]);
+        }
+      }
+      bar();
+      if (wt == 0) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float M = m[x], f[WT];
+#pragma unroll
+          for (int w = 1; w < WT; ++w) M = fmaxf(M, mlbuf[((w - 1) * C::kRows + row[x]) * 2]);
+          const float base = M == -INFINITY ? 0.f : M;
+          f[0] = fast_exp2(m[x] - base);
+          l[x] *= f[0];
+#pragma unroll
+          for (int w = 1; w < WT; ++w) {
+            const float* ml = mlbuf + ((w - 1) * C::kRows + row[x]) * 2;
+            f[w] = fast_exp2(ml[0] - base);
+            l[x] += f[w] * ml[1];
+          }
+          m[x] = M;
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            o[j][2 * x] *= f[0], o[j][2 * x + 1] *= f[0];
+#pragma unroll
+            for (int w = 1; w < WT; ++w) {
+              const float2 v = *reinterpret_cast<const float2*>(
+                  mbuf + ((w - 1) * C::kRows + row[x]) * C::kPitch + j * 8 + tq * 2);
+              o[j][2 * x] += f[w] * v.x, o[j][2 * x + 1] += f[w] * v.y;
+            }
+          }
+        }
+      }
+    }
+    // ---- whole row group: the result; else a partial, and the last CTA merges ----
+    if (wt == 0) {
+      const int rows_max = a.nodes_per_group * G;
+      float* slot = a.partial + int64_t(pc.slot) * tree_slot_floats(a);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (row[x] >= rows) continue;
+        if (pc.n_pieces == 1) {
+          const float inv = a.v_scale / l[x];
+          const int64_t at = (int64_t(pc.hd.b) * a.T + pc.node0 + row[x] / G) * a.num_q_heads + pc.hd.kv * G +
+                             row[x] % G;
+          uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + at * D);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) dst[j * 4 + tq] = pack_bf16x2(o[j][2 * x] * inv, o[j][2 * x + 1] * inv);
+          if (tq == 0 && a.lse) a.lse[at] = (m[x] + log2f(l[x])) * kTreeLn2;
+        } else {
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            *reinterpret_cast<float2*>(slot + row[x] * D + j * 8 + tq * 2) =
+                make_float2(o[j][2 * x], o[j][2 * x + 1]);
+          if (tq == 0)
+            *reinterpret_cast<float2*>(slot + rows_max * D + 2 * row[x]) = make_float2(m[x], l[x]);
+        }
+      }
+    }
+    if (pc.n_pieces > 1) {
+      __threadfence();
+      bar();
+      if (threadIdx.x == 0) s_last = tree_ticket(a, pc.head, pc.group, pc.n_pieces);
+      bar();
+      if (s_last) {
+        __threadfence();
+        tree_merge<__nv_bfloat16, D>(a, pc, threadIdx.x, NC * 32);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// fp32 pages: SIMT, FP32 FMA only.  At most 16 rows a group; the draft's rows
+// are read where they are.
+// ---------------------------------------------------------------------------
+constexpr int kF32Threads = 128;
+constexpr int kF32Rows = 16;
+
+template <int D, int P>
+__global__ void __launch_bounds__(kF32Threads) tree_f32_kernel(TreeLaunch a) {
+  using Split = TreeSplit<1, 4, 8>;
+  constexpr int ACC = kF32Rows * D / kF32Threads;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  float* kp = reinterpret_cast<float*>(smem);  // [P][D]
+  float* vp = kp + P * D;                      // [D][P]
+  float* qs = vp + P * D;                      // [rows][D]
+  float* sc = qs + kF32Rows * D;               // [rows][P]
+  float* st = sc + kF32Rows * P;               // alpha, m, l of each row
+  __shared__ int64_t scratch[kF32Threads / 32 + 2];
+  __shared__ int16_t par[kMaxTreeNodes];
+  __shared__ int pos[kF32Rows];
+  __shared__ uint64_t anc[kF32Rows];
+  __shared__ int s_last;
+  const int tid = threadIdx.x, G = a.group;
+  Split split;
+  if (!split.template init<kF32Threads>(a, scratch)) return;
+  typename Split::Walk walk = split.walk();
+  typename Split::Piece pc;
+  while (split.next(a, walk, pc)) {
+    __syncthreads();
+    if (tid < pc.n) par[tid] = tree_parent(a, pc.hd.b, tid);
+    __syncthreads();
+    const int rows = pc.nodes * G, rows_max = a.nodes_per_group * G;
+    const int64_t q0 = int64_t(pc.hd.b) * a.T + pc.node0;
+    auto at_row = [&](int r) { return (q0 + r / G) * a.num_q_heads + pc.hd.kv * G + r % G; };
+    if (tid < rows) {
+      int depth;
+      tree_node(par, pc.node0 + tid / G, pc.hd, depth, anc[tid]);
+      pos[tid] = pc.hd.ctx_len + depth;
+      st[kF32Rows + tid] = -INFINITY, st[2 * kF32Rows + tid] = 0.f;
+    }
+    for (int e = tid; e < rows * D; e += kF32Threads)
+      qs[e] = static_cast<const float*>(a.q)[at_row(e / D) * D + e % D];
+    float acc[ACC];
+#pragma unroll
+    for (int j = 0; j < ACC; ++j) acc[j] = 0.f;
+    for (int p = pc.p0; p < pc.p1; ++p) {
+      const bool draft = p >= pc.live;
+      const int first = (p - pc.live) * P;  // draft: the page's first node
+      PageDesc pg{};
+      if (!draft) {
+        pg = a.pages[pc.hd.vpage_begin + p];
+        if (slot_hi(pg) <= slot_lo(pg)) continue;
+        if (pg.phys < 0 || pg.phys >= a.pool_pages) {
+          if (tid == 0) record_error(a.status, kDevBadPage);
+          continue;
+        }
+      }
+      __syncthreads();
+      if (!draft) {
+        const uint4* ks = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.kpool) + pg.phys * a.page_bytes);
+        const uint4* vs = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.vpool) + pg.phys * a.page_bytes);
+        for (int e = tid; e < P * D / 4; e += kF32Threads) {
+          reinterpret_cast<uint4*>(kp)[e] = ks[e];
+          reinterpret_cast<uint4*>(vp)[e] = vs[e];
+        }
+      } else {
+        const int64_t base = int64_t(pc.hd.b) * a.ds_seq + int64_t(pc.hd.kv) * a.ds_head;
+        for (int e = tid; e < P * D; e += kF32Threads) {
+          const int t = e / D, i = e % D;
+          const int64_t from = base + (first + t) * a.ds_tok + i;
+          const bool in = first + t < pc.n;
+          kp[e] = in ? static_cast<const float*>(a.k_draft)[from] : 0.f;
+          vp[i * P + t] = in ? static_cast<const float*>(a.v_draft)[from] : 0.f;
+        }
+      }
+      __syncthreads();
+      for (int e = tid; e < rows * P; e += kF32Threads) {
+        const int r = e / P, t = e % P;
+        const uint64_t vis = draft ? anc[r] >> first : tree_page_mask(pg, pc.hd, pos[r]);
+        float s = 0.f;
+        for (int i = 0; i < D; ++i) s = fmaf(qs[r * D + i], kp[t * D + i], s);
+        sc[e] = (vis >> t) & 1 ? s * a.scale_log2 : -INFINITY;
+      }
+      __syncthreads();
+      if (tid < rows) {
+        float mx = -INFINITY;
+        for (int t = 0; t < P; ++t) mx = fmaxf(mx, sc[tid * P + t]);
+        const float mo = st[kF32Rows + tid], mn = fmaxf(mo, mx), base = mn == -INFINITY ? 0.f : mn;
+        const float al = exp2f(mo - base);
+        float sum = 0.f;
+        for (int t = 0; t < P; ++t) {
+          const float pv = exp2f(sc[tid * P + t] - base);
+          sc[tid * P + t] = pv;
+          sum += pv;
+        }
+        st[tid] = al;
+        st[kF32Rows + tid] = mn;
+        st[2 * kF32Rows + tid] = st[2 * kF32Rows + tid] * al + sum;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < ACC; ++j) {
+        const int e = tid + j * kF32Threads, r = e / D, col = e % D;
+        if (r >= rows) continue;
+        float x = acc[j] * st[r];
+        for (int t = 0; t < P; ++t) x = fmaf(sc[r * P + t], vp[col * P + t], x);
+        acc[j] = x;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < ACC; ++j) {
+      const int e = tid + j * kF32Threads, r = e / D, col = e % D;
+      if (r >= rows) continue;
+      const float M = st[kF32Rows + r], L = st[2 * kF32Rows + r];
+      if (pc.n_pieces == 1) {
+        static_cast<float*>(a.out)[at_row(r) * D + col] = acc[j] / L;
+        if (col == 0 && a.lse) a.lse[at_row(r)] = (M + log2f(L)) * kTreeLn2;
+      } else {
+        float* slot = a.partial + int64_t(pc.slot) * tree_slot_floats(a);
+        slot[r * D + col] = acc[j];
+        if (col == 0) slot[rows_max * D + 2 * r] = M, slot[rows_max * D + 2 * r + 1] = L;
+      }
+    }
+    if (pc.n_pieces > 1) {
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) s_last = tree_ticket(a, pc.head, pc.group, pc.n_pieces);
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        tree_merge<float, D>(a, pc, tid, kF32Threads);
+      }
+    }
+  }
+}
+
+template <int D, bool FP8, int WR, int WT>
+cudaError_t launch_mma(const TreeLaunch& a, cudaStream_t s) {
+  using C = TreeMma<D, FP8, WR, WT>;
+  auto kern = tree_mma_kernel<D, FP8, WR, WT>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
+  if (e != cudaSuccess) return e;
+  kern<<<a.n_ctas, C::kThreads, C::kBytes, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <int D, int P>
+cudaError_t launch_f32(const TreeLaunch& a, cudaStream_t s) {
+  const int bytes = (2 * P * D + kF32Rows * D + kF32Rows * P + 3 * kF32Rows) * 4;
+  auto kern = tree_f32_kernel<D, P>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  kern<<<a.n_ctas, kF32Threads, bytes, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <int D, bool FP8>
+cudaError_t launch_rows(const TreeLaunch& a, cudaStream_t s) {
+  return a.nodes_per_group * a.group <= 16 ? launch_mma<D, FP8, 1, 4>(a, s) : launch_mma<D, FP8, 4, 2>(a, s);
+}
+
+}  // namespace
+
+// Rows of a group: 16 (one query tile) while a sequence's rows fit, else 64.
+TreeConfig tree_config(const sp_plan* plan, int32_t nodes) {
+  const int g = plan->group;
+  TreeConfig c{};
+  const bool f32 = plan->prob.dtype == SP_F32;
+  const int rows = f32 || nodes * g <= 16 ? 16 : 64;
+  c.nodes_per_group = rows / g;
+  c.rows_per_group = c.nodes_per_group * g;
+  c.n_ctas = rows == 16 ? 2 * 148 : 148;
+  return c;
+}
+
+cudaError_t launch_tree(const TreeLaunch& a, const TreeConfig&, cudaStream_t s) {
+  if (!a.bf16) {
+    if (a.P == 16) return a.D == 128 ? launch_f32<128, 16>(a, s) : launch_f32<64, 16>(a, s);
+    return a.D == 128 ? launch_f32<128, 64>(a, s) : launch_f32<64, 64>(a, s);
+  }
+  if (a.fp8) return a.D == 128 ? launch_rows<128, true>(a, s) : launch_rows<64, true>(a, s);
+  return a.D == 128 ? launch_rows<128, false>(a, s) : launch_rows<64, false>(a, s);
+}
+
+}  // namespace sp

@@ -21,6 +21,7 @@ constexpr int kStatusBytes = 256;            // workspace prefix holding the sta
 constexpr int kPrefillTileTokensBf16 = 128;  // query tile of the tcgen05 prefill kernel
 constexpr int kPrefillTileTokensF32 = 64;    // KV / query tile of the fp32 prefill kernel
 constexpr int kMaxGroup = 16;                // q-heads per kv-head handled by one decode CTA
+constexpr int kMaxTreeNodes = 64;            // drafted nodes a sequence: one 64-bit ancestor mask, one page of 64
 
 // Floats of one decode partial-result slot: acc [G][D], then (m, l) per row in
 // a 4G-float block, so that every slot starts 16-byte aligned.
@@ -36,6 +37,8 @@ enum DeviceCode : int32_t {
   kDevBadPage = 5,         // a table page id outside [0, pool_pages): nothing read or written there
   kDevAppendFull = 6,      // an append found no reserved page left (ring plans)
   kDevPoolEmpty = 7,       // an append found the shared spare pool empty (ring plans with spare pages)
+  kDevBadTree = 8,         // a draft tree with a parent not before its node, a bad node count, path or node index
+  kDevBadParent = 9,       // a reorder from a sequence that does not exist or is laid out otherwise
 };
 
 // Shared spare pool of a ring plan (table section): word 0 holds how many of

@@ -1,0 +1,275 @@
+// Work split, visibility and merge of tree attention, shared by its kernels.
+//
+// A sequence's draft is a forest of n <= 64 nodes (parent[i] < i); node i at
+// depth d sits at position p = L + d, L the sequence's context length.  With
+// s the sink and w the window of a LOCAL head it sees, of the cache, the
+// positions j < s or j > p - w (a GLOBAL head: all; a RETRIEVAL head: its kept
+// blocks' pages too, which carry kSpanCausal), and of the draft itself
+// and its ancestors, by the same rule at their positions.  A kv-head's rows
+// are its nodes times its group's q-heads, node-major.
+//
+// Split.  A head's work is its live pages, then the draft's page(s), in tiles
+// of `TP` pages, once for each row group, plus a fixed cost per group
+// (kStartTiles: loading Q, publishing or writing the rows).  Laid end to end
+// over the heads this is a line of U units; CTA c of G takes [cU/G, (c+1)U/G).
+// Every CTA works the line out from the table itself (a block-wide sum over
+// the heads), so the split follows the lengths as the cache grows and needs no
+// host work and no list: which CTAs share a row group, and which workspace
+// slot each of them wrote (its first piece: 2c, a later one: 2c + 1; pieces
+// between cover their group and need none) are arithmetic on (U, G).
+#pragma once
+
+#include "append_common.cuh"
+#include "kernels.h"
+
+namespace sp {
+
+constexpr float kTreeLn2 = 0.6931471805599453f;
+
+// Bits [x, y) of a 64-bit word (any x, y).
+__device__ __forceinline__ uint64_t bit_range(int x, int y) {
+  x = max(x, 0), y = min(y, 64);
+  return y <= x ? 0 : (~uint64_t(0) >> (64 - (y - x))) << x;
+}
+
+// Slots of a cached page that a row at position p sees (p is behind the cache: no causal bound).
+__device__ __forceinline__ uint64_t tree_page_mask(const PageDesc& pg, const HeadDesc& hd, int p) {
+  const int lo = slot_lo(pg), hi = slot_hi(pg);
+  if (hd.kind == 0 || page_causal(pg)) return bit_range(lo, hi);
+  return bit_range(lo, min(hi, hd.sink - pg.abs_start)) | bit_range(max(lo, p - hd.window + 1 - pg.abs_start), hi);
+}
+// Does every row at a position <= p_last see all 64 slots of this page?
+__device__ __forceinline__ bool tree_page_full(const PageDesc& pg, const HeadDesc& hd, int p_last) {
+  if (slot_lo(pg) != 0 || slot_hi(pg) != 64) return false;
+  if (hd.kind == 0 || page_causal(pg)) return true;
+  return pg.abs_start + 63 < hd.sink || pg.abs_start > p_last - hd.window;
+}
+
+// Node count of sequence b, bounded; *bad reports one outside [0, T].
+__device__ __forceinline__ int tree_nodes(const TreeLaunch& a, int b, bool* bad = nullptr) {
+  if (!a.num_nodes) return a.T;
+  const int n = a.num_nodes[b];
+  if (bad && (n < 0 || n > a.T)) *bad = true;
+  return min(max(n, 0), a.T);
+}
+
+// Depth and ancestor mask (itself included, the head's local rule applied) of
+// node i; par holds the sequence's parents with every entry in [-1, own index).
+__device__ __forceinline__ void tree_node(const int16_t* par, int i, const HeadDesc& hd, int& depth, uint64_t& mask) {
+  depth = 0;
+  for (int x = par[i]; x >= 0; x = par[x]) ++depth;
+  mask = 0;
+  int d = depth;  // depth of x
+  for (int x = i; x >= 0; x = par[x], --d)
+    if (hd.kind == 0 || depth - d < hd.window || hd.ctx_len + d < hd.sink) mask |= uint64_t(1) << x;
+}
+
+// One parent entry, checked: an invalid one is reported and counts as a root.
+__device__ __forceinline__ int16_t tree_parent(const TreeLaunch& a, int b, int i) {
+  const int x = a.parents[int64_t(b) * a.T + i];
+  if (x >= -1 && x < i) return int16_t(x);
+  record_error(a.status, kDevBadTree);
+  return -1;
+}
+
+template <int TP, int START, int MIN_UNITS>
+struct TreeSplit {
+  static constexpr int kStartTiles = START;  // fixed cost of a row group, in tiles
+  int64_t units;                             // U
+  int32_t ctas;                              // G, <= the grid
+  int32_t head;                              // head the CTA's range starts in ...
+  int64_t head_unit;                         // ... and that head's first unit
+
+  struct Weight {
+    int32_t n;       // nodes of the sequence
+    int32_t live;    // cached page records to visit
+    int32_t pages;   // live + the draft's pages
+    int32_t groups;  // row groups
+    int64_t per;     // units of one row group
+  };
+  __device__ __forceinline__ static Weight weight(const TreeLaunch& a, int kind, int ctx_len, int n_vpages, int b) {
+    Weight w;
+    w.n = tree_nodes(a, b);
+    w.live = kind == 0 ? min(n_vpages, (ctx_len + a.P - 1) / a.P) : n_vpages;
+    w.pages = w.live + (w.n + a.P - 1) / a.P;
+    w.groups = (w.n + a.nodes_per_group - 1) / a.nodes_per_group;
+    w.per = (w.pages + TP - 1) / TP + START;
+    return w;
+  }
+  __device__ __forceinline__ static int64_t head_units(const TreeLaunch& a, int h) {
+    const HeadDesc* d = a.heads + h;
+    if (blockIdx.x == 0 && d->kv == 0) {
+      bool bad = false;
+      tree_nodes(a, d->b, &bad);
+      if (bad) record_error(a.status, kDevBadTree);
+    }
+    const Weight w = weight(a, d->kind, d->ctx_len, d->n_vpages, d->b);
+    return w.per * w.groups;
+  }
+  __device__ __forceinline__ int64_t cut(int64_t c) const { return c * units / ctas; }
+  __device__ __forceinline__ int cta_of(int64_t u) const { return int(((u + 1) * ctas + units - 1) / units) - 1; }
+
+  // All NT threads of the block.  scratch: NT / 32 + 2 int64 in shared memory.
+  // Returns false when this CTA has no work.
+  template <int NT>
+  __device__ bool init(const TreeLaunch& a, int64_t* scratch) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int NW = NT / 32;
+    auto scan = [&](int64_t v, int64_t& total) {  // inclusive sum over the block
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += x;
+      }
+      if (lane == 31) scratch[warp] = v;
+      __syncthreads();
+      int64_t before = 0;
+      total = 0;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        if (i < warp) before += scratch[i];
+        total += scratch[i];
+      }
+      __syncthreads();
+      return v + before;
+    };
+    int64_t sum = 0, mine = 0, upto = 0;
+    for (int h0 = 0; h0 < a.n_heads; h0 += NT) {
+      const int h = h0 + int(threadIdx.x);
+      mine = h < a.n_heads ? head_units(a, h) : 0;
+      int64_t total;
+      upto = sum + scan(mine, total);
+      sum += total;
+    }
+    units = sum;
+    ctas = int(min(int64_t(gridDim.x), max(int64_t(1), sum / MIN_UNITS)));
+    if (sum == 0 || int(blockIdx.x) >= ctas) return false;
+    const int64_t u0 = cut(blockIdx.x);
+    int64_t run = 0;
+    for (int h0 = 0; h0 < a.n_heads; h0 += NT) {
+      if (a.n_heads > NT) {  // more than one round: sum again, this time to find the head
+        const int h = h0 + int(threadIdx.x);
+        mine = h < a.n_heads ? head_units(a, h) : 0;
+        int64_t total;
+        upto = run + scan(mine, total);
+        run += total;
+      }
+      if (u0 < upto && u0 >= upto - mine) scratch[NW] = h0 + int(threadIdx.x), scratch[NW + 1] = upto - mine;
+    }
+    __syncthreads();
+    head = int32_t(scratch[NW]);
+    head_unit = scratch[NW + 1];
+    return true;
+  }
+
+  struct Piece {
+    HeadDesc hd;
+    int32_t head, group;
+    int32_t n;             // nodes of the sequence
+    int32_t node0, nodes;  // the row group's nodes
+    int32_t live;          // cached records; page index >= live: draft page
+    int32_t p0, p1;        // pages [p0, p1) of live + draft
+    int32_t n_pieces;      // CTAs sharing the row group
+    int32_t first_cta;     // the first of them
+    int32_t first_slot;    // its slot
+    int32_t slot;          // this piece's slot
+  };
+  struct Walk {
+    int64_t u, u1, head_unit;
+    int32_t head;
+  };
+  __device__ __forceinline__ Walk walk() const {
+    return Walk{cut(blockIdx.x), cut(blockIdx.x + 1), head_unit, head};
+  }
+  // The CTA's next piece (uniform over the threads); false: no more.
+  __device__ __forceinline__ bool next(const TreeLaunch& a, Walk& w, Piece& pc) const {
+    while (w.u < w.u1) {
+      pc.hd = a.heads[w.head];
+      const Weight g = weight(a, pc.hd.kind, pc.hd.ctx_len, pc.hd.n_vpages, pc.hd.b);
+      const int64_t local = w.u - w.head_unit, end = g.per * g.groups;
+      if (local >= end) {
+        w.head_unit += end;
+        ++w.head;
+        continue;
+      }
+      const int32_t group = int32_t(local / g.per);
+      const int64_t x = local - group * g.per, y = min(g.per, x + (w.u1 - w.u));
+      const int64_t at = w.u - x;  // the row group's first unit
+      w.u += y - x;
+      if (y <= START) continue;  // only the fixed cost falls into this CTA: the next one takes all pages
+      pc.head = w.head;
+      pc.group = group;
+      pc.n = g.n;
+      pc.node0 = group * a.nodes_per_group;
+      pc.nodes = min(a.nodes_per_group, g.n - pc.node0);
+      pc.live = g.live;
+      pc.p0 = int32_t(max(int64_t(0), x - START) * TP);
+      pc.p1 = int32_t(min(int64_t(g.pages), (y - START) * TP));
+      pc.first_cta = cta_of(at + START);
+      pc.n_pieces = cta_of(at + g.per - 1) - pc.first_cta + 1;
+      pc.first_slot = 2 * pc.first_cta + (cut(pc.first_cta) < at ? 1 : 0);
+      pc.slot = int(blockIdx.x) == pc.first_cta ? pc.first_slot : 2 * int(blockIdx.x);
+      return true;
+    }
+    return false;
+  }
+};
+
+// Floats of a partial slot: acc [rows][D], then (m, l) of each row; 16-byte aligned.
+__device__ __forceinline__ int64_t tree_slot_floats(const TreeLaunch& a) {
+  return partial_slot_floats(a.nodes_per_group * a.group, a.D);
+}
+
+template <typename T>
+__device__ __forceinline__ void tree_store4(T* dst, float4 v) {
+  if constexpr (sizeof(T) == 2)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+  else
+    *reinterpret_cast<float4*>(dst) = v;
+}
+
+// Merge of a shared row group, by the CTA that published last: for each row
+// O = sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i, pieces in line order
+// (a fixed order: the same bits whichever CTA is last).  Threads tid, tid + nt, ...
+template <typename T, int D, typename Piece>
+__device__ __forceinline__ void tree_merge(const TreeLaunch& a, const Piece& pc, int tid, int nt) {
+  const int64_t stride = tree_slot_floats(a);
+  const int rows_max = a.nodes_per_group * a.group, rows = pc.nodes * a.group;
+  auto slot = [&](int i) {
+    return a.partial + int64_t(i == 0 ? pc.first_slot : 2 * (pc.first_cta + i)) * stride;
+  };
+  for (int e = tid; e < rows * (D / 4); e += nt) {
+    const int row = e / (D / 4), col = (e % (D / 4)) * 4;
+    float M = -INFINITY;
+    for (int i = 0; i < pc.n_pieces; ++i) M = fmaxf(M, __ldcg(slot(i) + rows_max * D + 2 * row));
+    const float base = M == -INFINITY ? 0.f : M;
+    float l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < pc.n_pieces; ++i) {
+      const float* s = slot(i);
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(s + rows_max * D + 2 * row));
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(s + row * D + col));
+      const float f = exp2f(ml.x - base);
+      l += f * ml.y;
+      acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
+    }
+    const float inv = a.v_scale / l;
+    const int64_t at = (int64_t(pc.hd.b) * a.T + pc.node0 + row / a.group) * a.num_q_heads + pc.hd.kv * a.group +
+                       row % a.group;
+    tree_store4(static_cast<T*>(a.out) + at * D + col,
+                make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+    if (col == 0 && a.lse) a.lse[at] = (M + log2f(l)) * kTreeLn2;
+  }
+}
+
+// Ticket of a published piece (one thread, after the block's stores and a
+// fence): true for the last of the group's CTAs, which returns the counter to zero.
+__device__ __forceinline__ bool tree_ticket(const TreeLaunch& a, int head, int group, int n_pieces) {
+  int32_t* c = a.counters + int64_t(head) * kMaxTreeNodes + group;
+  if (atomicAdd(c, 1) != n_pieces - 1) return false;
+  *c = 0;
+  return true;
+}
+
+}  // namespace sp

@@ -14,6 +14,14 @@ import torch
 from . import segpaged as S
 
 
+def _on(device: torch.device, stream):
+    """Context: ``stream`` (a torch stream, a raw handle, or None: the device's current stream) is current."""
+    if stream is None:
+        return torch.cuda.stream(torch.cuda.current_stream(device))
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else
+                             torch.cuda.ExternalStream(int(stream), device=device))
+
+
 def _stream(stream) -> int:
     if stream is None:
         return torch.cuda.current_stream().cuda_stream
@@ -59,6 +67,7 @@ class SegPagedLayer:
         else:
             self.k_pool, self.v_pool = pools
         self.workspace = torch.zeros(z.workspace_bytes, dtype=torch.uint8, device=self.device)
+        self.tree_workspaces: list[torch.Tensor] = []  # of tree_attention; the last is in use
 
     # -- argument checks (the C ABI sees only pointers and strides) ------------
     def _check_tensor(self, t: torch.Tensor, what: str, dtype: torch.dtype) -> None:
@@ -173,8 +182,110 @@ class SegPagedLayer:
                                self.workspace.numel(), _stream(stream))
         return out, lse
 
+    # -- several candidates a sequence -------------------------------------------
+    def prepare_tree(self, max_nodes: int) -> None:
+        """Allocate the workspace of ``tree_attention`` for trees of up to ``max_nodes`` nodes.
+
+        A call makes it when it is missing; a CUDA graph capture needs it made before.  Workspaces
+        that a larger one replaced are kept: a captured graph may hold their addresses."""
+        need = S.segpaged_tree_workspace(self.plan, max_nodes)
+        if not self.tree_workspaces or self.tree_workspaces[-1].numel() < need:
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("call prepare_tree(max_nodes) before a CUDA graph capture")
+            self.tree_workspaces.append(torch.zeros(need, dtype=torch.uint8, device=self.device))
+            torch.cuda.current_stream(self.device).synchronize()  # zeroed before any stream's call uses it
+
+    def _check_draft(self, k: torch.Tensor, v: torch.Tensor, nodes: int) -> None:
+        self._check_tensor(k, "k_draft", self.torch_dtype)
+        self._check_tensor(v, "v_draft", self.torch_dtype)
+        want = (self.batch, nodes, self.num_kv_heads, self.head_dim)
+        if tuple(k.shape) != want or k.shape != v.shape or k.stride() != v.stride() or k.stride(-1) != 1:
+            raise ValueError(f"k_draft / v_draft must be {want} with the same strides, head_dim contiguous; got "
+                             f"{tuple(k.shape)} and {tuple(v.shape)}")
+
+    def _check_index(self, t: torch.Tensor, what: str, *shape: int) -> None:
+        self._check_tensor(t, what, torch.int32)
+        if tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous {shape}, got {tuple(t.shape)}")
+
+    def tree_attention(self, q: torch.Tensor, k_draft: torch.Tensor, v_draft: torch.Tensor, parents: torch.Tensor,
+                       num_nodes: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                       lse: torch.Tensor | None = None, scale: float = 0.0, stream=None):
+        """Attention of a drafted tree a sequence over the cache and over the draft itself.
+
+        ``q``: contiguous [B, T, Hq, d], one row a node; ``k_draft`` / ``v_draft``: [B, T, Hkv, d], the
+        nodes' own keys and values (not in the cache); ``parents``: int32 [B, T], -1 for a root, else an
+        earlier node; ``num_nodes``: int32 [B] or None (T each).  Node i at depth d stands at position
+        L + d and sees the cache by its head's rule, its ancestors and itself.  Returns (out, lse); rows
+        behind ``num_nodes[b]`` are left as they were (in fresh outputs: zero).  T is at most 64."""
+        self._check_tensor(q, "q", self.torch_dtype)
+        if q.dim() != 4 or q.shape[0] != self.batch or tuple(q.shape[2:]) != (self.num_q_heads, self.head_dim) or \
+                not q.is_contiguous() or not 1 <= q.shape[1] <= S.SP_TREE_MAX_NODES:
+            raise ValueError(f"q must be contiguous [{self.batch}, 1 .. {S.SP_TREE_MAX_NODES}, {self.num_q_heads}, "
+                             f"{self.head_dim}], got {tuple(q.shape)}")
+        T = q.shape[1]
+        rows = tuple(q.shape[:3])
+        self._check_draft(k_draft, v_draft, T)
+        self._check_index(parents, "parents", self.batch, T)
+        if num_nodes is not None:
+            self._check_index(num_nodes, "num_nodes", self.batch)
+        with _on(self.device, stream):  # fresh outputs and workspaces belong to the call's stream
+            fresh = torch.empty_like if num_nodes is None else torch.zeros_like
+            out = fresh(q) if out is None else out
+            self._check_tensor(out, "out", self.torch_dtype)
+            if out.shape != q.shape or not out.is_contiguous():
+                raise ValueError(f"out must be contiguous {tuple(q.shape)}, got {tuple(out.shape)}")
+            lse = fresh(q[..., 0], dtype=torch.float32, memory_format=torch.contiguous_format) if lse is None else lse
+            self._check_tensor(lse, "lse", torch.float32)
+            if tuple(lse.shape) != rows or not lse.is_contiguous():
+                raise ValueError(f"lse must be contiguous {rows}, got {tuple(lse.shape)}")
+            self.prepare_tree(T)
+            ws = self.tree_workspaces[-1]
+            S.segpaged_tree_attention(self.plan, self.table.data_ptr(), self.k_pool.data_ptr(), self.v_pool.data_ptr(),
+                                      q.data_ptr(), k_draft.data_ptr(), v_draft.data_ptr(), k_draft.stride(0),
+                                      k_draft.stride(1), k_draft.stride(2), parents.data_ptr(),
+                                      num_nodes.data_ptr() if num_nodes is not None else None, T, out.data_ptr(),
+                                      lse.data_ptr(), scale, ws.data_ptr(), ws.numel(), _stream(None))
+        return out, lse
+
+    def tree_commit(self, k_draft: torch.Tensor, v_draft: torch.Tensor, path: torch.Tensor, path_len: torch.Tensor,
+                    stream=None) -> None:
+        """Ring plans: append the accepted nodes ``path[b, :path_len[b]]`` of the draft to each sequence.
+
+        ``k_draft`` / ``v_draft`` as in ``tree_attention``; ``path``: int32 [B, M], ``path_len``: int32 [B]
+        in [0, M].  The cache ends as after that many ``append`` calls."""
+        if not isinstance(k_draft, torch.Tensor) or k_draft.dim() != 4:
+            raise ValueError("k_draft must be a [B, T, Hkv, d] tensor")
+        self._check_draft(k_draft, v_draft, k_draft.shape[1])
+        if not isinstance(path, torch.Tensor) or path.dim() != 2:
+            raise ValueError("path must be an int32 [B, M] tensor")
+        self._check_index(path, "path", self.batch, path.shape[1])
+        self._check_index(path_len, "path_len", self.batch)
+        with _on(self.device, stream):
+            S.segpaged_tree_commit(self.plan, self.table.data_ptr(), k_draft.data_ptr(), v_draft.data_ptr(),
+                                   k_draft.stride(0), k_draft.stride(1), k_draft.stride(2), k_draft.shape[1],
+                                   path.data_ptr(), path_len.data_ptr(), path.shape[1], self.k_pool.data_ptr(),
+                                   self.v_pool.data_ptr(), self.workspace.data_ptr(), _stream(None))
+
+    def reorder(self, parents: torch.Tensor, common_len: torch.Tensor | None = None, stream=None) -> None:
+        """Ring plans: sequence b goes on with the cache of sequence ``parents[b]`` (int32 [B]), in place.
+
+        Forks, beam reorderings, any map; ``common_len`` (int32 [B]): positions below it are known equal in
+        both and not copied.  b and ``parents[b]`` need the same policies and ``ctx_len`` page counts."""
+        self._check_index(parents, "parents", self.batch)
+        if common_len is not None:
+            self._check_index(common_len, "common_len", self.batch)
+        with _on(self.device, stream):
+            S.segpaged_reorder(self.plan, self.table.data_ptr(), parents.data_ptr(),
+                               common_len.data_ptr() if common_len is not None else None, self.k_pool.data_ptr(),
+                               self.v_pool.data_ptr(), self.workspace.data_ptr(), _stream(None))
+
     def device_status(self, stream=None) -> int:
-        return S.segpaged_read_device_status(self.workspace.data_ptr(), _stream(stream))
+        """The first recorded code of the layer's workspaces (0: none)."""
+        code = S.segpaged_read_device_status(self.workspace.data_ptr(), _stream(stream))
+        for ws in self.tree_workspaces:
+            code = code or S.segpaged_read_device_status(ws.data_ptr(), _stream(stream))
+        return code
 
     def close(self) -> None:
         if getattr(self, "plan", None):

@@ -34,7 +34,8 @@ EXPORTED = ("segpaged_plan_create", "segpaged_plan_destroy", "segpaged_plan_size
             "segpaged_attention_decode_noalloc", "segpaged_decode_append", "segpaged_decode_step",
             "segpaged_read_device_status",
             "segpaged_clear_device_status", "segpaged_eval_exp2_fma", "segpaged_block_mass_workspace",
-            "segpaged_block_mass", "segpaged_status_string", "segpaged_last_error", "segpaged_abi_version")
+            "segpaged_block_mass", "segpaged_tree_workspace", "segpaged_tree_attention", "segpaged_tree_commit",
+            "segpaged_reorder", "segpaged_status_string", "segpaged_last_error", "segpaged_abi_version")
 
 
 class SegPagedError(RuntimeError):
@@ -117,6 +118,11 @@ def load(path: Path | str | None = None) -> ctypes.CDLL:
         "segpaged_block_mass_workspace": ([ctypes.POINTER(sp_problem), ctypes.POINTER(sz)], i32),
         "segpaged_block_mass": ([ctypes.POINTER(sp_problem), vp, i64, i64, i64, vp, ctypes.c_float, vp, i64, vp,
                                  sz, vp], i32),
+        "segpaged_tree_workspace": ([vp, i32, ctypes.POINTER(sz)], i32),
+        "segpaged_tree_attention": ([vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, vp, vp, i32, vp, vp, ctypes.c_float,
+                                     vp, sz, vp], i32),
+        "segpaged_tree_commit": ([vp, vp, vp, vp, i64, i64, i64, i32, vp, vp, i32, vp, vp, vp, vp], i32),
+        "segpaged_reorder": ([vp, vp, vp, vp, vp, vp, vp, vp], i32),
         "segpaged_status_string": ([i32], ctypes.c_char_p),
         "segpaged_last_error": ([], ctypes.c_char_p),
         "segpaged_abi_version": ([], i32),
@@ -361,6 +367,42 @@ def segpaged_block_mass(problem: sp_problem, k_dense: int, stride_seq: int, stri
 def segpaged_block_mass_status(problem: sp_problem, *args) -> int:
     """Like segpaged_block_mass but returns the status code instead of raising."""
     return load().segpaged_block_mass(ctypes.byref(problem), *args)
+
+
+SP_TREE_MAX_NODES = 64
+
+
+def segpaged_tree_workspace(plan: int, max_nodes: int) -> int:
+    """Workspace bytes segpaged_tree_attention needs for trees of up to ``max_nodes`` nodes."""
+    n = ctypes.c_size_t()
+    _check(load().segpaged_tree_workspace(plan, max_nodes, ctypes.byref(n)), "segpaged_tree_workspace")
+    return n.value
+
+
+def segpaged_tree_attention(plan: int, d_table: int, k_pool: int, v_pool: int, q: int, k_draft: int, v_draft: int,
+                            stride_seq: int, stride_tok: int, stride_head: int, parents: int, num_nodes: int | None,
+                            nodes: int, out: int, lse: int | None, softmax_scale: float, workspace: int,
+                            workspace_bytes: int, stream: int = 0) -> None:
+    """Attention of each sequence's drafted tree over its cache and over the draft itself."""
+    _check(load().segpaged_tree_attention(plan, d_table, k_pool, v_pool, q, k_draft, v_draft, stride_seq, stride_tok,
+                                          stride_head, parents, num_nodes, nodes, out, lse, softmax_scale, workspace,
+                                          workspace_bytes, stream), "segpaged_tree_attention")
+
+
+def segpaged_tree_commit(plan: int, d_table: int, k_draft: int, v_draft: int, stride_seq: int, stride_tok: int,
+                         stride_head: int, nodes: int, path: int, path_len: int, max_path: int, k_pool: int,
+                         v_pool: int, workspace: int, stream: int = 0) -> None:
+    """Append each sequence's accepted path to a ring plan's cache, in place (device table updated)."""
+    _check(load().segpaged_tree_commit(plan, d_table, k_draft, v_draft, stride_seq, stride_tok, stride_head, nodes,
+                                       path, path_len, max_path, k_pool, v_pool, workspace, stream),
+           "segpaged_tree_commit")
+
+
+def segpaged_reorder(plan: int, d_table: int, parents: int, common_len: int | None, k_pool: int, v_pool: int,
+                     workspace: int, stream: int = 0) -> None:
+    """Give each sequence of a ring plan the cache of sequence ``parents[b]``, in place."""
+    _check(load().segpaged_reorder(plan, d_table, parents, common_len, k_pool, v_pool, workspace, stream),
+           "segpaged_reorder")
 
 
 def segpaged_abi_version() -> int:

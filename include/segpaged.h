@@ -432,6 +432,96 @@ SP_API sp_status segpaged_decode_step(const sp_plan* plan, void* d_table, const 
                                       const void* q, void* out, float* lse, float softmax_scale, void* workspace,
                                       size_t workspace_bytes, void* stream);
 
+/* ---- decoding several candidates --------------------------------------------
+ * The pages decode one token a sequence and step; the three calls below serve
+ * decoding that holds several candidates over the same head-aware cache: a
+ * tree of drafted tokens attended in one call, the accepted path joining the
+ * cache, and sequences taking over other sequences' caches (forked samples,
+ * beams).  They follow the head kinds' own rules ("SegPagedAttention runtime
+ * design", §1, §3; "RedKnot head classification").
+ *
+ * segpaged_tree_attention: queries of drafted nodes over the cache of a decode
+ * plan and over the draft itself.  Sequence b's draft is a forest of n =
+ * num_nodes[b] nodes, each after its parent; node i at depth d (a root: 0)
+ * stands at position p = L + d, L the sequence's context length as held by the
+ * device table: the draft's tokens are not in the cache.  Node i sees
+ *   of the cache, [0, L): every position (GLOBAL, DENSE), or the positions
+ *     j < sink or j > p - window (LOCAL), and those of the kept blocks
+ *     (RETRIEVAL);
+ *   of the draft, itself and its ancestors, by the same rule at their
+ *     positions (RETRIEVAL: as LOCAL); never another branch.
+ * With a chain of nodes this is decode attention of consecutive tokens, and a
+ * node's result is that of the decode call made after committing its path.
+ *   q        device [batch, nodes, num_q_heads, head_dim], dtype of the plan
+ *   k_draft, v_draft  device: element (b, i, kv, x) at base + b*stride_seq +
+ *            i*stride_tok + kv*stride_head + x (16-byte aligned rows), dtype of
+ *            the plan; must hold finite values in rows below num_nodes[b].
+ *            With SP_E4M3 pages each row counts as the codes that the cache
+ *            will hold for it
+ *   parents  device int32 [batch, nodes]: -1 for a root, else below i
+ *   num_nodes device int32 [batch] in [0, nodes], or NULL: nodes each
+ *   nodes    1 .. 64 (more: SP_ERR_UNSUPPORTED)
+ *   out, lse as q, and fp32 [batch, nodes, num_q_heads] or NULL.  Rows at and
+ *            behind num_nodes[b] are not read (q, draft, parents) nor written
+ *   softmax_scale  <= 0 selects 1/sqrt(head_dim)
+ *   workspace device, 256-byte aligned, at least what segpaged_tree_workspace
+ *            gives for `nodes` or more; zero-filled before its first use (and
+ *            after a device status, before it is used again).  It begins with a
+ *            status block of its own (segpaged_read_device_status).  Calls that
+ *            overlap on the GPU need separate workspaces.
+ * All decode plans, ring plans or not, every dtype and page type.  One launch; no atomics on results: the same inputs give the same
+ * bits.  A parent not in [-1, i), or a num_nodes outside [0, nodes], is found
+ * on the device: status code 8; the node then counts as a root, the count as
+ * the nearest one in range. */
+SP_API sp_status segpaged_tree_workspace(const sp_plan* plan, int32_t max_nodes, size_t* bytes);
+SP_API sp_status segpaged_tree_attention(const sp_plan* plan, const void* d_table, const void* k_pool,
+                                         const void* v_pool, const void* q, const void* k_draft, const void* v_draft,
+                                         int64_t stride_seq, int64_t stride_tok, int64_t stride_head,
+                                         const int32_t* parents, const int32_t* num_nodes, int32_t nodes, void* out,
+                                         float* lse, float softmax_scale, void* workspace, size_t workspace_bytes,
+                                         void* stream);
+
+/* segpaged_tree_commit: the accepted path of each sequence joins a ring plan's
+ * cache, in place: the nodes path[b][0 .. path_len[b]) of the draft are
+ * appended in that order at positions L, L + 1, ...  Pools and table end as
+ * after path_len[b] calls of segpaged_decode_append with those rows, bit for
+ * bit (a head without room keeps what fits and reports code 6 or 7, as there).
+ *   k_draft, v_draft, strides, nodes  as segpaged_tree_attention
+ *   path      device int32 [batch, max_path], node indices in [0, nodes)
+ *   path_len  device int32 [batch] in [0, max_path]; 0 leaves a sequence as it is
+ *   max_path  1 .. 64
+ *   workspace the plan's (segpaged_plan_sizes), for the status word
+ * A length or node index outside its range leaves the whole sequence as it is
+ * and reports code 8.  The path need not follow the tree's edges: which nodes
+ * were accepted is the caller's decision. */
+SP_API sp_status segpaged_tree_commit(const sp_plan* plan, void* d_table, const void* k_draft, const void* v_draft,
+                                      int64_t stride_seq, int64_t stride_tok, int64_t stride_head, int32_t nodes,
+                                      const int32_t* path, const int32_t* path_len, int32_t max_path, void* k_pool,
+                                      void* v_pool, void* workspace, void* stream);
+
+/* segpaged_reorder: sequence b of a ring plan goes on with the cache of
+ * sequence parents[b], for all b at once and in place: forks (one parent of
+ * several), beam reorderings, rotations, any map.  Whole pages are copied into
+ * the pages that b's heads own, only those that hold a token, and b's context
+ * lengths and page records become its parent's; a GLOBAL head that needs more
+ * pages than it has takes them from the spare pool, and keeps those it no
+ * longer needs for its own growth.
+ *   parents     device int32 [batch]; parents[b] == b leaves b as it is
+ *   common_len  device int32 [batch] or NULL.  The caller vouches that b and
+ *               parents[b] hold equal tokens at the positions below
+ *               common_len[b] (a shared prompt): pages that hold only such
+ *               positions are not copied.  With E4M3 pages: equal codes
+ *   workspace   the plan's (segpaged_plan_sizes), for the status word
+ * b and parents[b] must be laid out alike: the same head kinds, sinks, windows
+ * and number of page records (ctx_len + append_capacity of the plan).  One
+ * that is not, or an index outside [0, batch), leaves sequence b as it is and
+ * reports code 9.  When the spare pool runs out (code 7) or a page id is
+ * invalid (code 5), the contents of the sequences concerned are undefined.
+ * batch <= 2048, num_kv_heads <= 1024 (else SP_ERR_UNSUPPORTED). */
+SP_API sp_status segpaged_reorder(const sp_plan* plan, void* d_table, const int32_t* parents,
+                                  const int32_t* common_len, void* k_pool, void* v_pool, void* workspace,
+                                  void* stream);
+
 /* Device status word.  The pages have no counterpart: this is the failure
  * detection of this library's kernels.  Kernels never trap; a failed
  * device-side check or a bounded wait that ran out records a non-zero code in
@@ -442,6 +532,9 @@ SP_API sp_status segpaged_decode_step(const sp_plan* plan, void* d_table, const 
  *         kernel read or wrote nothing there (a corrupted table)
  *   6     a ring append found no reserved page left (the append was skipped)
  *   7     a ring append found the shared spare pool empty (the append was skipped)
+ *   8     a drafted tree with a parent not before its node, or a node count, a
+ *         path length or a path's node index outside its range
+ *   9     a reorder from a sequence that does not exist or is laid out otherwise
  * read synchronises `stream`, copies the word to *code (host) and returns
  * SP_OK for 0, SP_ERR_DEVICE_CHECK for a recorded code (SP_ERR_CUDA if the
  * synchronisation or the copy fails); clear zeroes the word's 256-byte block
