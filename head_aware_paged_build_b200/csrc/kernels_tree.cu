@@ -34,8 +34,7 @@ struct TreeMma {
   static constexpr int kDescOff = kMlOff + (WT - 1) * kRows * 2 * 4;
   static constexpr int kBarOff = kDescOff + kStages * 16;
   static constexpr int kScanOff = kBarOff + 2 * kStages * 8;
-  static constexpr int kParOff = kScanOff + (kConsumers + 1 + 2) * 8;
-  static constexpr int kBytes = kParOff + kMaxTreeNodes * 2 + 16;
+  static constexpr int kBytes = kScanOff + (kConsumers + 1 + 2) * 8;
   using Split = TreeSplit<1, 4, 8>;
 };
 
@@ -54,7 +53,6 @@ __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
   uint64_t* empty = full + NST;
   int64_t* scratch = reinterpret_cast<int64_t*>(smem + C::kScanOff);
-  int16_t* par = reinterpret_cast<int16_t*>(smem + C::kParOff);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -94,14 +92,7 @@ __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 
         }
         uint8_t* kd = stage + s * 2 * PB;
         if (p >= pc.live) {  // the draft's page
-          for (int e = lane; e < 2 * PB / 16; e += 32) reinterpret_cast<uint4*>(kd)[e] = make_uint4(0, 0, 0, 0);
-          __syncwarp();
-          const int64_t base = int64_t(pc.hd.b) * a.ds_seq + int64_t(pc.hd.kv) * a.ds_head;
-          const __nv_bfloat16* kn = static_cast<const __nv_bfloat16*>(a.k_draft) + base;
-          const __nv_bfloat16* vn = static_cast<const __nv_bfloat16*>(a.v_draft) + base;
-          for (int t = 0; t < pc.n; ++t)
-            append_write_token<__nv_bfloat16, D, P, FP8>(kn + t * a.ds_tok, vn + t * a.ds_tok, kd, kd + PB, t,
-                                                         a.k_inv, a.v_inv, lane, 32);
+          tree_draft_page<D, FP8>(a, pc.hd, pc.n, kd, P * 128, kd + PB, lane);
           fence_proxy_async_smem();  // before a later bulk copy into this stage
           __syncwarp();
           if (lane == 0) {
@@ -138,9 +129,8 @@ __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 
   const int row[2] = {wr * 16 + grp, wr * 16 + grp + 8};
   bool ok = true;
   while (split.next(a, walk, pc)) {
-    bar();  // every warp is done with the previous piece's parents and merge buffers
-    if (threadIdx.x < pc.n) par[threadIdx.x] = tree_parent(a, pc.hd.b, threadIdx.x);
-    bar();
+    uint64_t nodes[2];
+    tree_ancestors(a, pc.hd.b, pc.n, lane, nodes);
     const int rows = pc.nodes * G;
     const int p_last = pc.hd.ctx_len + pc.n - 1;
     int pos[2] = {0, 0};
@@ -150,10 +140,10 @@ __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       qrow[x] = nullptr;
+      const uint64_t mask = tree_mask_of(nodes, min(pc.node0 + row[x] / G, kMaxTreeNodes - 1));
       if (row[x] < rows) {
-        int depth;
-        tree_node(par, pc.node0 + row[x] / G, pc.hd, depth, anc[x]);
-        pos[x] = pc.hd.ctx_len + depth;
+        anc[x] = tree_visible(mask, pc.hd);
+        pos[x] = pc.hd.ctx_len + __popcll(mask) - 1;
         qrow[x] = static_cast<const __nv_bfloat16*>(a.q) +
                   ((int64_t(pc.hd.b) * a.T + pc.node0 + row[x] / G) * a.num_q_heads + pc.hd.kv * G + row[x] % G) * D;
       }
@@ -297,6 +287,7 @@ __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 
       l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
     }
     if constexpr (WT > 1) {
+      bar();  // the previous piece's buffers are read
       if (wt > 0) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -394,7 +385,6 @@ __global__ void __launch_bounds__(kF32Threads) tree_f32_kernel(TreeLaunch a) {
   float* sc = qs + kF32Rows * D;               // [rows][P]
   float* st = sc + kF32Rows * P;               // alpha, m, l of each row
   __shared__ int64_t scratch[kF32Threads / 32 + 2];
-  __shared__ int16_t par[kMaxTreeNodes];
   __shared__ int pos[kF32Rows];
   __shared__ uint64_t anc[kF32Rows];
   __shared__ int s_last;
@@ -405,16 +395,18 @@ __global__ void __launch_bounds__(kF32Threads) tree_f32_kernel(TreeLaunch a) {
   typename Split::Piece pc;
   while (split.next(a, walk, pc)) {
     __syncthreads();
-    if (tid < pc.n) par[tid] = tree_parent(a, pc.hd.b, tid);
-    __syncthreads();
     const int rows = pc.nodes * G, rows_max = a.nodes_per_group * G;
     const int64_t q0 = int64_t(pc.hd.b) * a.T + pc.node0;
     auto at_row = [&](int r) { return (q0 + r / G) * a.num_q_heads + pc.hd.kv * G + r % G; };
-    if (tid < rows) {
-      int depth;
-      tree_node(par, pc.node0 + tid / G, pc.hd, depth, anc[tid]);
-      pos[tid] = pc.hd.ctx_len + depth;
-      st[kF32Rows + tid] = -INFINITY, st[2 * kF32Rows + tid] = 0.f;
+    if (tid < 32) {  // one warp holds all rows' nodes
+      uint64_t nodes[2];
+      tree_ancestors(a, pc.hd.b, pc.n, tid, nodes);
+      const uint64_t mask = tree_mask_of(nodes, min(pc.node0 + tid / G, kMaxTreeNodes - 1));
+      if (tid < rows) {
+        anc[tid] = tree_visible(mask, pc.hd);
+        pos[tid] = pc.hd.ctx_len + __popcll(mask) - 1;
+        st[kF32Rows + tid] = -INFINITY, st[2 * kF32Rows + tid] = 0.f;
+      }
     }
     for (int e = tid; e < rows * D; e += kF32Threads)
       qs[e] = static_cast<const float*>(a.q)[at_row(e / D) * D + e % D];
@@ -535,17 +527,19 @@ cudaError_t launch_f32(const TreeLaunch& a, cudaStream_t s) {
 
 template <int D, bool FP8>
 cudaError_t launch_rows(const TreeLaunch& a, cudaStream_t s) {
-  return a.nodes_per_group * a.group <= 16 ? launch_mma<D, FP8, 1, 4>(a, s) : launch_mma<D, FP8, 4, 2>(a, s);
+  const int rows = a.nodes_per_group * a.group;
+  if (rows <= 16) return launch_mma<D, FP8, 1, 4>(a, s);
+  return rows <= 32 ? launch_mma<D, FP8, 2, 4>(a, s) : launch_mma<D, FP8, 4, 2>(a, s);
 }
 
 }  // namespace
 
-// Rows of a group: 16 (one query tile) while a sequence's rows fit, else 64.
+// Rows of a group: 16 or 32 while a sequence's rows fit, else 64.
 TreeConfig tree_config(const sp_plan* plan, int32_t nodes) {
   const int g = plan->group;
   TreeConfig c{};
   const bool f32 = plan->prob.dtype == SP_F32;
-  const int rows = f32 || nodes * g <= 16 ? 16 : 64;
+  const int rows = f32 || nodes * g <= 16 ? 16 : nodes * g <= 32 ? 32 : 64;
   c.nodes_per_group = rows / g;
   c.rows_per_group = c.nodes_per_group * g;
   c.n_ctas = rows == 16 ? 2 * 148 : 148;

@@ -53,23 +53,138 @@ __device__ __forceinline__ int tree_nodes(const TreeLaunch& a, int b, bool* bad 
   return min(max(n, 0), a.T);
 }
 
-// Depth and ancestor mask (itself included, the head's local rule applied) of
-// node i; par holds the sequence's parents with every entry in [-1, own index).
-__device__ __forceinline__ void tree_node(const int16_t* par, int i, const HeadDesc& hd, int& depth, uint64_t& mask) {
-  depth = 0;
-  for (int x = par[i]; x >= 0; x = par[x]) ++depth;
-  mask = 0;
-  int d = depth;  // depth of x
-  for (int x = i; x >= 0; x = par[x], --d)
-    if (hd.kind == 0 || depth - d < hd.window || hd.ctx_len + d < hd.sink) mask |= uint64_t(1) << x;
+// Ancestor masks (each node itself included) of a sequence's n nodes, by one
+// warp: lane x holds nodes x and x + 32.  Pointer doubling: a round joins each
+// node's mask with that of the farthest ancestor reached so far and jumps
+// there, so a chain of 64 takes six rounds and a shallow tree one or two.  An
+// entry outside [-1, own index) is reported and counts as a root.
+__device__ __forceinline__ void tree_ancestors(const TreeLaunch& a, int b, int n, int lane, uint64_t (&anc)[2]) {
+  int up[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int i = lane + 32 * x;
+    up[x] = -1;
+    anc[x] = uint64_t(1) << i;
+    if (i < n) {
+      const int p = a.parents[int64_t(b) * a.T + i];
+      if (p < -1 || p >= i) record_error(a.status, kDevBadTree);
+      else up[x] = p;
+    }
+  }
+  while (__any_sync(0xffffffffu, up[0] >= 0 || up[1] >= 0)) {
+    uint64_t m[2];
+    int next[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int from = up[x] & 31;
+      const uint64_t m0 = __shfl_sync(0xffffffffu, anc[0], from), m1 = __shfl_sync(0xffffffffu, anc[1], from);
+      const int u0 = __shfl_sync(0xffffffffu, up[0], from), u1 = __shfl_sync(0xffffffffu, up[1], from);
+      m[x] = up[x] < 0 ? 0 : up[x] >= 32 ? m1 : m0;
+      next[x] = up[x] < 0 ? -1 : up[x] >= 32 ? u1 : u0;
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) anc[x] |= m[x], up[x] = next[x];
+  }
+}
+// Node i's mask out of the warp's (all lanes call; i may differ by lane).
+__device__ __forceinline__ uint64_t tree_mask_of(const uint64_t (&anc)[2], int i) {
+  const uint64_t m0 = __shfl_sync(0xffffffffu, anc[0], i & 31), m1 = __shfl_sync(0xffffffffu, anc[1], i & 31);
+  return i >= 32 ? m1 : m0;
+}
+// The ancestors a node sees: a node's index is above its parent's, so the k-th
+// set bit is the ancestor at depth k, and a LOCAL head hides the lowest bits
+// that are neither in the window nor among the sink positions.
+__device__ __forceinline__ uint64_t tree_visible(uint64_t mask, const HeadDesc& hd) {
+  const int depth = __popcll(mask) - 1;
+  if (hd.kind == 0 || hd.window > depth) return mask;
+  uint64_t left = mask, hidden = 0;
+  for (int d = 0; d <= depth - hd.window; ++d) {
+    const uint64_t bit = left & (0 - left);
+    left ^= bit;
+    if (hd.ctx_len + d >= hd.sink) hidden |= bit;
+  }
+  return mask & ~hidden;
 }
 
-// One parent entry, checked: an invalid one is reported and counts as a root.
-__device__ __forceinline__ int16_t tree_parent(const TreeLaunch& a, int b, int i) {
-  const int x = a.parents[int64_t(b) * a.T + i];
-  if (x >= -1 && x < i) return int16_t(x);
-  record_error(a.status, kDevBadTree);
-  return -1;
+// One warp writes the draft's n rows as a page of 64 slots in shared memory:
+// K in blocks of 64 dimensions k_block bytes apart (bf16; E4M3 pages are one
+// block), V transposed, both as an append lays them out; slots behind n hold
+// zeros in V (their weights are zero, and 0 x garbage must stay 0) and are left
+// as they are in K (their scores are masked).  Loads go out in batches: the
+// rows come from global memory, and one row at a time would cost its latency
+// up to 64 times.
+template <int D, bool FP8>
+__device__ __forceinline__ void tree_draft_page(const TreeLaunch& a, const HeadDesc& hd, int n, uint8_t* kdst,
+                                                int k_block, uint8_t* vdst, int lane) {
+  const int64_t base = int64_t(hd.b) * a.ds_seq + int64_t(hd.kv) * a.ds_head;
+  const __nv_bfloat16* kn = static_cast<const __nv_bfloat16*>(a.k_draft) + base;
+  const __nv_bfloat16* vn = static_cast<const __nv_bfloat16*>(a.v_draft) + base;
+  constexpr int CR = D / 8, KB = 8;  // 16-byte chunks of a K row; loads in flight
+  for (int u0 = lane; u0 < n * CR; u0 += 32 * KB) {
+    uint4 v[KB];
+#pragma unroll
+    for (int i = 0; i < KB; ++i) {
+      const int u = u0 + 32 * i;
+      if (u < n * CR) v[i] = *reinterpret_cast<const uint4*>(kn + (u / CR) * a.ds_tok + (u % CR) * 8);
+    }
+#pragma unroll
+    for (int i = 0; i < KB; ++i) {
+      const int u = u0 + 32 * i, t = u / CR, c = u % CR;
+      if (u >= n * CR) continue;
+      if constexpr (FP8) {
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        uint32_t q[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t lo = w[2 * h], hi = w[2 * h + 1];
+          q[h] = uint32_t(pack_e4m3x2(__uint_as_float(lo << 16) * a.k_inv,
+                                      __uint_as_float(lo & 0xffff0000u) * a.k_inv)) |
+                 uint32_t(pack_e4m3x2(__uint_as_float(hi << 16) * a.k_inv,
+                                      __uint_as_float(hi & 0xffff0000u) * a.k_inv))
+                     << 16;
+        }
+        *reinterpret_cast<uint2*>(kdst + fp8_kpage_offset(t, c * 8, D)) = make_uint2(q[0], q[1]);
+      } else {
+        *reinterpret_cast<uint4*>(kdst + (c >> 3) * k_block + t * 128 + (((c & 7) ^ (t & 7)) << 4)) = v[i];
+      }
+    }
+  }
+  // V: a lane takes two dimensions of a run of tokens and writes a 16-byte chunk of each
+  constexpr int DP = D / 2, TG = FP8 ? 16 : 8;
+#pragma unroll 2
+  for (int u = lane; u < DP * (64 / TG); u += 32) {
+    const int i = (u % DP) * 2, g = u / DP;
+    uint32_t x[TG];
+#pragma unroll
+    for (int e = 0; e < TG; ++e) {
+      const int t = g * TG + (FP8 ? fp8_vpos_tok(e) : e);
+      x[e] = t < n ? *reinterpret_cast<const uint32_t*>(vn + t * a.ds_tok + i) : 0u;
+    }
+    uint32_t lo[4], hi[4];  // dimension i, dimension i + 1
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      if constexpr (FP8) {
+        uint32_t c[2] = {0, 0};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t p = x[4 * w + 2 * h], r = x[4 * w + 2 * h + 1];
+          c[0] |= uint32_t(pack_e4m3x2(__uint_as_float(p << 16) * a.v_inv, __uint_as_float(r << 16) * a.v_inv))
+                  << (16 * h);
+          c[1] |= uint32_t(pack_e4m3x2(__uint_as_float(p & 0xffff0000u) * a.v_inv,
+                                       __uint_as_float(r & 0xffff0000u) * a.v_inv))
+                  << (16 * h);
+        }
+        lo[w] = c[0], hi[w] = c[1];
+      } else {
+        lo[w] = __byte_perm(x[2 * w], x[2 * w + 1], 0x5410);
+        hi[w] = __byte_perm(x[2 * w], x[2 * w + 1], 0x7632);
+      }
+    }
+    const int64_t o0 = FP8 ? fp8_vpage_offset(i, g * 16) : vpage_chunk_offset_bf16(i, g);
+    const int64_t o1 = FP8 ? fp8_vpage_offset(i + 1, g * 16) : vpage_chunk_offset_bf16(i + 1, g);
+    *reinterpret_cast<uint4*>(vdst + o0) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    *reinterpret_cast<uint4*>(vdst + o1) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+  }
 }
 
 template <int TP, int START, int MIN_UNITS>
