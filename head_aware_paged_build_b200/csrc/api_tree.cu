@@ -104,7 +104,7 @@ sp_status segpaged_tree_attention(const sp_plan* plan, const void* d_table, cons
   L.scale_log2 = softmax_scale_of(plan, softmax_scale) * 1.4426950408889634f * plan->k_scale;
   L.v_scale = plan->v_scale;
   L.k_inv = 1.0f / plan->k_scale, L.v_inv = 1.0f / plan->v_scale;
-  L.nodes_per_group = c.nodes_per_group, L.n_ctas = c.n_ctas;
+  L.nodes_per_group = c.nodes_per_group, L.nodes_per_tile = c.nodes_per_tile, L.n_ctas = c.n_ctas;
   L.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + tree_partial_offset(plan));
   L.counters = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + kStatusBytes);
   L.status = static_cast<int32_t*>(workspace);

@@ -177,6 +177,7 @@ struct TreeLaunch {
   float v_scale;       // E4M3 pages: value scale, applied to the normalised output
   float k_inv, v_inv;  // E4M3 pages: 1 / k_scale, 1 / v_scale (the draft's rows are quantised as the append does)
   int32_t nodes_per_group;  // nodes whose rows (nodes x group) one work item takes
+  int32_t nodes_per_tile;   // tcgen05 kernel: nodes of a 128-row query tile (one or two tiles a group)
   int32_t n_ctas;
   float* partial;     // workspace slots, two for each CTA
   int32_t* counters;  // workspace arrival counters, kMaxTreeNodes for each head (zero between calls)
@@ -186,11 +187,13 @@ struct TreeLaunch {
 struct TreeConfig {
   bool tensor;  // the tcgen05 kernel (bf16 pages)
   int32_t nodes_per_group;
+  int32_t nodes_per_tile;
   int32_t rows_per_group;  // nodes_per_group * group
   int32_t n_ctas;
 };
 TreeConfig tree_config(const sp_plan* plan, int32_t nodes);
 cudaError_t launch_tree(const TreeLaunch& a, const TreeConfig& c, cudaStream_t s);
+cudaError_t launch_tree_tc(const TreeLaunch& a, cudaStream_t s);
 
 // Appending the accepted path of each sequence (segpaged_tree_commit).
 struct CommitLaunch {

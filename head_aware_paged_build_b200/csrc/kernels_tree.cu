@@ -11,12 +11,13 @@
 // on m16n8k16 fragments.  Scores, sums and O are fp32; P is rounded to the
 // type of the pages' operands (bf16, or f16 over widened E4M3 codes), V's own
 // type, while the sums use the unrounded weights.
+#include <algorithm>
+
 #include "tree_common.cuh"
 
 namespace sp {
 namespace {
 
-constexpr int kDraftPage = -2;  // phys of the draft's page in a stage's record
 constexpr float kLazyLog2 = 8.f;
 
 template <int D, bool FP8, int WR, int WT>
@@ -534,19 +535,30 @@ cudaError_t launch_rows(const TreeLaunch& a, cudaStream_t s) {
 
 }  // namespace
 
-// Rows of a group: 16 or 32 while a sequence's rows fit, else 64.
+// Rows of a group: 16 or 32 while a sequence's rows fit; more rows of bf16
+// pages go to the tensor cores in tiles of 128, two at a time where a sequence
+// has more; else 64.
 TreeConfig tree_config(const sp_plan* plan, int32_t nodes) {
-  const int g = plan->group;
+  const int g = plan->group, all = nodes * g;
   TreeConfig c{};
-  const bool f32 = plan->prob.dtype == SP_F32;
-  const int rows = f32 || nodes * g <= 16 ? 16 : nodes * g <= 32 ? 32 : 64;
-  c.nodes_per_group = rows / g;
+  c.tensor = plan->prob.dtype == SP_BF16 && !plan->fp8 && all > 32;
+  c.nodes_per_tile = 128 / g;
+  int most;
+  if (c.tensor) {
+    most = (all > 128 ? 2 : 1) * c.nodes_per_tile;
+    c.n_ctas = 148;
+  } else {
+    const int rows = plan->prob.dtype == SP_F32 || all <= 16 ? 16 : all <= 32 ? 32 : 64;
+    most = rows / g;
+    c.n_ctas = rows == 16 ? 2 * 148 : 148;
+  }
+  c.nodes_per_group = std::min(most, nodes);
   c.rows_per_group = c.nodes_per_group * g;
-  c.n_ctas = rows == 16 ? 2 * 148 : 148;
   return c;
 }
 
-cudaError_t launch_tree(const TreeLaunch& a, const TreeConfig&, cudaStream_t s) {
+cudaError_t launch_tree(const TreeLaunch& a, const TreeConfig& c, cudaStream_t s) {
+  if (c.tensor) return launch_tree_tc(a, s);
   if (!a.bf16) {
     if (a.P == 16) return a.D == 128 ? launch_f32<128, 16>(a, s) : launch_f32<64, 16>(a, s);
     return a.D == 128 ? launch_f32<128, 64>(a, s) : launch_f32<64, 64>(a, s);

@@ -24,6 +24,7 @@
 
 namespace sp {
 
+constexpr int kDraftPage = -2;  // phys of the draft's page in a stage's record
 constexpr float kTreeLn2 = 0.6931471805599453f;
 
 // Bits [x, y) of a 64-bit word (any x, y).
