@@ -22,17 +22,14 @@ T* section(const void* d_table, int64_t off) {
   return reinterpret_cast<T*>(const_cast<uint8_t*>(static_cast<const uint8_t*>(d_table)) + off);
 }
 
-// Workspace: status block | arrival counters (the same place whatever the
-// tree's size, so that calls of different sizes leave each other's at zero) |
-// two partial slots for each CTA.
-int64_t tree_partial_offset(const sp_plan* plan) {
-  return kStatusBytes + (int64_t(plan->hdr.n_heads) * kMaxTreeNodes * 4 + 255) / 256 * 256;
-}
+// Workspace: status block | descriptions of split row groups, one a CTA | two
+// partial slots a CTA.
+constexpr int64_t kTreePartialOffset = kStatusBytes + (kTreeMaxCtas * int64_t(sizeof(TreeJoin)) + 255) / 256 * 256;
 
 int64_t tree_workspace_bytes(const sp_plan* plan, int32_t nodes) {
   const TreeConfig c = tree_config(plan, nodes);
   const int64_t slot = partial_slot_floats(c.rows_per_group, plan->prob.head_dim) * 4;
-  return tree_partial_offset(plan) + (2 * int64_t(c.n_ctas) * slot + 255) / 256 * 256;
+  return kTreePartialOffset + (2 * int64_t(c.n_ctas) * slot + 255) / 256 * 256;
 }
 
 sp_status check_tree_plan(const sp_plan* plan, int32_t nodes) {
@@ -105,10 +102,11 @@ sp_status segpaged_tree_attention(const sp_plan* plan, const void* d_table, cons
   L.v_scale = plan->v_scale;
   L.k_inv = 1.0f / plan->k_scale, L.v_inv = 1.0f / plan->v_scale;
   L.nodes_per_group = c.nodes_per_group, L.nodes_per_tile = c.nodes_per_tile, L.n_ctas = c.n_ctas;
-  L.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + tree_partial_offset(plan));
-  L.counters = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + kStatusBytes);
+  L.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kTreePartialOffset);
+  L.joins = reinterpret_cast<TreeJoin*>(static_cast<uint8_t*>(workspace) + kStatusBytes);
   L.status = static_cast<int32_t*>(workspace);
-  const cudaError_t e = launch_tree(L, c, static_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_tree(L, c, static_cast<cudaStream_t>(stream));
+  if (e == cudaSuccess) e = launch_tree_join(L, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SP_OK : cuda_fail(e, "segpaged_tree_attention launch");
 }
 

@@ -155,6 +155,16 @@ cudaError_t launch_block_mass(const BlockMassLaunch& a, cudaStream_t s);
 // (segpaged_tree_attention).  The work split is made on the device, from the
 // context lengths in the table (tree_common.cuh): the launch only says how a
 // kernel tiles its rows.
+constexpr int kTreeMaxCtas = 2 * 148 + 24;  // a multiple of 32
+// A row group whose pieces lie in several CTAs, kept by the one it starts in:
+// piece 0 is in slot first_slot, piece i in slot 2 (first CTA + i).
+struct alignas(16) TreeJoin {
+  int32_t n_pieces;  // 0: no group starts here and goes on
+  int32_t first_slot;
+  int32_t rows;
+  int32_t b, kv, node0;
+  int32_t pad[2];
+};
 struct TreeLaunch {
   const HeadDesc* heads;
   const PageDesc* pages;
@@ -180,7 +190,7 @@ struct TreeLaunch {
   int32_t nodes_per_tile;   // tcgen05 kernel: nodes of a 128-row query tile (one or two tiles a group)
   int32_t n_ctas;
   float* partial;     // workspace slots, two for each CTA
-  int32_t* counters;  // workspace arrival counters, kMaxTreeNodes for each head (zero between calls)
+  TreeJoin* joins;    // workspace, one for each CTA
   int32_t* status;
 };
 // How a kernel tiles a call: which kernel, its row group and its grid.
@@ -194,6 +204,7 @@ struct TreeConfig {
 TreeConfig tree_config(const sp_plan* plan, int32_t nodes);
 cudaError_t launch_tree(const TreeLaunch& a, const TreeConfig& c, cudaStream_t s);
 cudaError_t launch_tree_tc(const TreeLaunch& a, cudaStream_t s);
+cudaError_t launch_tree_join(const TreeLaunch& a, cudaStream_t s);
 
 // Appending the accepted path of each sequence (segpaged_tree_commit).
 struct CommitLaunch {

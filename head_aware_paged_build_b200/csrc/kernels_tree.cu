@@ -46,7 +46,6 @@ __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 
   constexpr int P = 64, PB = C::kPageBytes, NST = C::kStages, NC = C::kConsumers;
   constexpr int KSTEPS = D / 16, NT = D / 8, CHUNKS = 4 / WT;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ int s_last;
   uint8_t* stage = smem;
   float* mbuf = reinterpret_cast<float*>(smem + C::kMergeOff);
   float* mlbuf = reinterpret_cast<float*>(smem + C::kMlOff);
@@ -330,7 +329,7 @@ __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 
         }
       }
     }
-    // ---- whole row group: the result; else a partial, and the last CTA merges ----
+    // ---- whole row group: the result; else a partial ----
     if (wt == 0) {
       const int rows_max = a.nodes_per_group * G;
       float* slot = a.partial + int64_t(pc.slot) * tree_slot_floats(a);
@@ -355,16 +354,7 @@ __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 
         }
       }
     }
-    if (pc.n_pieces > 1) {
-      __threadfence();
-      bar();
-      if (threadIdx.x == 0) s_last = tree_ticket(a, pc.head, pc.group, pc.n_pieces);
-      bar();
-      if (s_last) {
-        __threadfence();
-        tree_merge<__nv_bfloat16, D>(a, pc, threadIdx.x, NC * 32);
-      }
-    }
+    if (threadIdx.x == 0) tree_note_join(a, pc);
   }
 }
 
@@ -388,7 +378,6 @@ __global__ void __launch_bounds__(kF32Threads) tree_f32_kernel(TreeLaunch a) {
   __shared__ int64_t scratch[kF32Threads / 32 + 2];
   __shared__ int pos[kF32Rows];
   __shared__ uint64_t anc[kF32Rows];
-  __shared__ int s_last;
   const int tid = threadIdx.x, G = a.group;
   Split split;
   if (!split.template init<kF32Threads>(a, scratch)) return;
@@ -493,16 +482,7 @@ __global__ void __launch_bounds__(kF32Threads) tree_f32_kernel(TreeLaunch a) {
         if (col == 0) slot[rows_max * D + 2 * r] = M, slot[rows_max * D + 2 * r + 1] = L;
       }
     }
-    if (pc.n_pieces > 1) {
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) s_last = tree_ticket(a, pc.head, pc.group, pc.n_pieces);
-      __syncthreads();
-      if (s_last) {
-        __threadfence();
-        tree_merge<float, D>(a, pc, tid, kF32Threads);
-      }
-    }
+    if (tid == 0) tree_note_join(a, pc);
   }
 }
 

@@ -82,7 +82,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
   uint64_t *s_full = bars + 4, *p_full = bars + 6, *kv_full = bars + 8, *kv_free = kv_full + NS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(kv_free + NS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* last_flag = abort_flag + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -479,16 +478,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         }
       }
       tc::fence_before_sync();
-      if (!whole) __threadfence();
       bar();  // both streams have read O and the exchanged statistics
-      if (!whole) {
-        if (t256 == 0) *last_flag = tree_ticket(a, pc.head, pc.group, pc.n_pieces);
-        bar();
-        if (*last_flag) {
-          __threadfence();
-          tree_merge<__nv_bfloat16, D>(a, pc, t256, kSoftmaxThreads);
-        }
-      }
+      if (t256 == 0) tree_note_join(a, pc);
       k += nt, ++pi;
     }
   }

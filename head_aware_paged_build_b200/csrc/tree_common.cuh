@@ -16,7 +16,9 @@
 // the heads), so the split follows the lengths as the cache grows and needs no
 // host work and no list: which CTAs share a row group, and which workspace
 // slot each of them wrote (its first piece: 2c, a later one: 2c + 1; pieces
-// between cover their group and need none) are arithmetic on (U, G).
+// between cover their group and need none) are arithmetic on (U, G).  A group
+// in one CTA is written there; the others' pieces are joined by a second,
+// dependent kernel.
 #pragma once
 
 #include "append_common.cuh"
@@ -226,9 +228,11 @@ struct TreeSplit {
   __device__ __forceinline__ int cta_of(int64_t u) const { return int(((u + 1) * ctas + units - 1) / units) - 1; }
 
   // All NT threads of the block.  scratch: NT / 32 + 2 int64 in shared memory.
-  // Returns false when this CTA has no work.
+  // Returns false when this CTA has no work.  Also lets the joining kernel's blocks be placed.
   template <int NT>
   __device__ bool init(const TreeLaunch& a, int64_t* scratch) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (threadIdx.x == 0) a.joins[blockIdx.x].n_pieces = 0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int NW = NT / 32;
     auto scan = [&](int64_t v, int64_t& total) {  // inclusive sum over the block
@@ -336,56 +340,14 @@ __device__ __forceinline__ int64_t tree_slot_floats(const TreeLaunch& a) {
   return partial_slot_floats(a.nodes_per_group * a.group, a.D);
 }
 
-template <typename T>
-__device__ __forceinline__ void tree_store4(T* dst, float4 v) {
-  if constexpr (sizeof(T) == 2)
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-  else
-    *reinterpret_cast<float4*>(dst) = v;
-}
-
-// Merge of a shared row group, by the CTA that published last: for each row
-// O = sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i, pieces in line order
-// (a fixed order: the same bits whichever CTA is last).  Threads tid, tid + nt, ...
-template <typename T, int D, typename Piece>
-__device__ __forceinline__ void tree_merge(const TreeLaunch& a, const Piece& pc, int tid, int nt) {
-  const int64_t stride = tree_slot_floats(a);
-  const int rows_max = a.nodes_per_group * a.group, rows = pc.nodes * a.group;
-  auto slot = [&](int i) {
-    return a.partial + int64_t(i == 0 ? pc.first_slot : 2 * (pc.first_cta + i)) * stride;
-  };
-  for (int e = tid; e < rows * (D / 4); e += nt) {
-    const int row = e / (D / 4), col = (e % (D / 4)) * 4;
-    float M = -INFINITY;
-    for (int i = 0; i < pc.n_pieces; ++i) M = fmaxf(M, __ldcg(slot(i) + rows_max * D + 2 * row));
-    const float base = M == -INFINITY ? 0.f : M;
-    float l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i < pc.n_pieces; ++i) {
-      const float* s = slot(i);
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(s + rows_max * D + 2 * row));
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(s + row * D + col));
-      const float f = exp2f(ml.x - base);
-      l += f * ml.y;
-      acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
-    }
-    const float inv = a.v_scale / l;
-    const int64_t at = (int64_t(pc.hd.b) * a.T + pc.node0 + row / a.group) * a.num_q_heads + pc.hd.kv * a.group +
-                       row % a.group;
-    tree_store4(static_cast<T*>(a.out) + at * D + col,
-                make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-    if (col == 0 && a.lse) a.lse[at] = (M + log2f(l)) * kTreeLn2;
-  }
-}
-
-// Ticket of a published piece (one thread, after the block's stores and a
-// fence): true for the last of the group's CTAs, which returns the counter to zero.
-__device__ __forceinline__ bool tree_ticket(const TreeLaunch& a, int head, int group, int n_pieces) {
-  int32_t* c = a.counters + int64_t(head) * kMaxTreeNodes + group;
-  if (atomicAdd(c, 1) != n_pieces - 1) return false;
-  *c = 0;
-  return true;
+// What the joining kernel needs of this CTA: the row group that starts in it
+// and goes on in the next one (a CTA starts one such group at most: its last
+// piece's).  One thread, at every piece; n_pieces 0: none.
+template <typename Piece>
+__device__ __forceinline__ void tree_note_join(const TreeLaunch& a, const Piece& pc) {
+  if (pc.n_pieces == 1 || pc.first_cta != int(blockIdx.x)) return;
+  a.joins[blockIdx.x] =
+      TreeJoin{pc.n_pieces, pc.first_slot, pc.nodes * a.group, pc.hd.b, pc.hd.kv, pc.node0, {0, 0}};
 }
 
 }  // namespace sp

@@ -465,11 +465,12 @@ SP_API sp_status segpaged_decode_step(const sp_plan* plan, void* d_table, const 
  *            behind num_nodes[b] are not read (q, draft, parents) nor written
  *   softmax_scale  <= 0 selects 1/sqrt(head_dim)
  *   workspace device, 256-byte aligned, at least what segpaged_tree_workspace
- *            gives for `nodes` or more; zero-filled before its first use (and
- *            after a device status, before it is used again).  It begins with a
- *            status block of its own (segpaged_read_device_status).  Calls that
- *            overlap on the GPU need separate workspaces.
- * All decode plans, ring plans or not, every dtype and page type.  One launch; no atomics on results: the same inputs give the same
+ *            gives for `nodes` or more.  It begins with a status block of its
+ *            own (segpaged_read_device_status), zero before the first use.
+ *            Calls that overlap on the GPU need separate workspaces.
+ * All decode plans, ring plans or not, every dtype and page type.  Two launches
+ * on `stream` (the attention, and a programmatic dependent of it that joins rows
+ * split over the GPU); fixed summation orders: the same inputs give the same
  * bits.  A parent not in [-1, i), or a num_nodes outside [0, nodes], is found
  * on the device: status code 8; the node then counts as a root, the count as
  * the nearest one in range. */
