@@ -1,16 +1,17 @@
 // Attention of a drafted tree over the paged cache: the mma.sync kernel
 // (E4M3 pages, and small row counts on bf16 pages) and the fp32 kernel.
 //
-// mma.sync kernel: a producer warp streams the piece's pages into a ring of
-// shared-memory stages with bulk copies, as decode does, and writes the
-// draft's rows as one more page of the same layout (E4M3 pages: quantised as
-// an append would, so a node sees exactly the codes the cache will hold once
-// the node is committed).  WR x WT consumer warps: warp (wr, wt) holds rows
-// 16 wr .. 16 wr + 15 of the row group and takes 64 / WT of each page's
-// tokens, 16 at a time: S = Q K^T, online softmax with a lazy rescale, O += P V
-// on m16n8k16 fragments.  Scores, sums and O are fp32; P is rounded to the
-// type of the pages' operands (bf16, or f16 over widened E4M3 codes), V's own
-// type, while the sums use the unrounded weights.
+// mma.sync kernel: a producer warp walks the CTA's pieces, hands each to the
+// others a slot ahead (its table entries, parents and Q rows) and streams its
+// pages into a ring of shared-memory stages with bulk copies, as decode does;
+// one or two more warps write the draft's rows as one more page of the same
+// layout (E4M3 pages: quantised as an append would, so a node sees exactly the
+// codes the cache will hold once the node is committed).  WR x WT consumer
+// warps: warp (wr, wt) holds rows 16 wr .. 16 wr + 15 of the row group and
+// takes 64 / WT of each page's tokens, 16 at a time: S = Q K^T, online softmax
+// with a lazy rescale, O += P V on m16n8k16 fragments.  Scores, sums and O are
+// fp32; P is rounded to the type of the pages' operands (bf16, or f16 over
+// widened E4M3 codes), V's own type, while the sums use the unrounded weights.
 #include <algorithm>
 
 #include "tree_common.cuh"
@@ -23,83 +24,124 @@ constexpr float kLazyLog2 = 8.f;
 template <int D, bool FP8, int WR, int WT>
 struct TreeMma {
   static constexpr int kConsumers = WR * WT;
-  static constexpr int kThreads = (kConsumers + 1) * 32;
+  // 16-row form: two CTAs an SM, whose 12 warps may have 168 registers a thread; a 14th would cost 40 of them
+  static constexpr int kDraftWarps = WR > 1 ? 2 : 1;
+  static constexpr int kThreads = (kConsumers + 1 + kDraftWarps) * 32;
   static constexpr int kRows = 16 * WR;
   static constexpr int kPageBytes = 64 * D * (FP8 ? 1 : 2);
-  static constexpr int kStages = (WR > 1 ? 128 : 64) * 1024 / (2 * kPageBytes) < 8
-                                     ? (WR > 1 ? 128 : 64) * 1024 / (2 * kPageBytes)
-                                     : 8;
+  static constexpr int kRing = (WR > 1 ? 128 : 64) * 1024 / (2 * kPageBytes);
+  static constexpr int kStages = kRing < 8 ? kRing : 8;
   static constexpr int kPitch = D + 8;
+  static constexpr int kQPitch = D * 2 + 16;  // bytes; the 8 rows of a fragment load fall on distinct banks
   static constexpr int kMergeOff = kStages * 2 * kPageBytes;
   static constexpr int kMlOff = kMergeOff + (WT - 1) * kRows * kPitch * 4;
-  static constexpr int kDescOff = kMlOff + (WT - 1) * kRows * 2 * 4;
+  static constexpr int kQOff = kMlOff + (WT - 1) * kRows * 2 * 4;
+  static constexpr int kDescOff = kQOff + 2 * kRows * kQPitch;
   static constexpr int kBarOff = kDescOff + kStages * 16;
-  static constexpr int kScanOff = kBarOff + 2 * kStages * 8;
-  static constexpr int kBytes = kScanOff + (kConsumers + 1 + 2) * 8;
-  using Split = TreeSplit<1, 4, 8>;
+  static constexpr int kScanOff = kBarOff + (2 * kStages + 6) * 8;
+  static constexpr int kInfoOff = kScanOff + ((kThreads / 32 + 2) * 8 + 15) / 16 * 16;
+  using Split = TreeSplit<1, 4, 2>;
+  using Info = TreePieceInfo<typename Split::Piece>;
+  static_assert(kMlOff % 8 == 0 && kQOff % 16 == 0 && kDescOff % 16 == 0 && kBarOff % 8 == 0 && kScanOff % 8 == 0 &&
+                    kInfoOff % alignof(Info) == 0,
+                "alignment of the shared-memory parts");
+  static constexpr int kBytes = kInfoOff + 2 * int(sizeof(Info));
 };
 
 template <int D, bool FP8, int WR, int WT>
 __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 : 2) tree_mma_kernel(TreeLaunch a) {
   using C = TreeMma<D, FP8, WR, WT>;
   using Split = typename C::Split;
-  constexpr int P = 64, PB = C::kPageBytes, NST = C::kStages, NC = C::kConsumers;
+  using Info = typename C::Info;
+  constexpr int P = 64, PB = C::kPageBytes, NST = C::kStages, NC = C::kConsumers, ND = C::kDraftWarps;
   constexpr int KSTEPS = D / 16, NT = D / 8, CHUNKS = 4 / WT;
+  constexpr uint32_t kAll = 0xffffffffu;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* stage = smem;
   float* mbuf = reinterpret_cast<float*>(smem + C::kMergeOff);
   float* mlbuf = reinterpret_cast<float*>(smem + C::kMlOff);
+  uint8_t* qbuf = smem + C::kQOff;
   PageDesc* sdesc = reinterpret_cast<PageDesc*>(smem + C::kDescOff);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
-  uint64_t* empty = full + NST;
+  uint64_t *empty = full + NST, *piece_full = empty + NST, *piece_free = piece_full + 2, *draft_go = piece_free + 2;
   int64_t* scratch = reinterpret_cast<int64_t*>(smem + C::kScanOff);
+  Info* info = reinterpret_cast<Info*>(smem + C::kInfoOff);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < NST; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 1 + ND);  // the producer and the draft's writers (it arrives for them on cached pages)
       mbar_init(&empty[s], NC);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&piece_full[s], 1);
+      mbar_init(&piece_free[s], NC + ND);
+      mbar_init(&draft_go[s], 1);
     }
     fence_barrier_init();
   }
   Split split;
   if (!split.template init<C::kThreads>(a, scratch)) return;  // its barriers order the mbarriers' init too
-  typename Split::Walk walk = split.walk();
-  typename Split::Piece pc;
+  const int G = a.group;
   int k = 0;  // pages streamed so far
 
   if (warp == NC) {
     // ------------------------------ producer ------------------------------
+    typename Split::Walk walk = split.walk();
+    typename Split::Piece pc;
     const uint8_t* kpool = static_cast<const uint8_t*>(a.kpool);
     const uint8_t* vpool = static_cast<const uint8_t*>(a.vpool);
     bool ok = true;
+    int pi = 0;
+    auto piece_slot = [&] {  // the next piece's slot, once it is free
+      const int ps = pi & 1;
+      ok = pi < 2 || __shfl_sync(kAll, int(lane == 0 && mbar_wait(&piece_free[ps], ((pi >> 1) - 1) & 1)), 0);
+      if (!ok && lane == 0) record_error(a.status, kDevTimeoutEmpty);
+      return ps;
+    };
     while (ok && split.next(a, walk, pc)) {
       const PageDesc* rec = a.pages + pc.hd.vpage_begin;
       int4 mine = make_int4(0, 0, 0, 0);
-      for (int p = pc.p0; ok && p < pc.p1; ++p, ++k) {
+      if (pc.p0 + lane < pc.live) mine = *reinterpret_cast<const int4*>(rec + pc.p0 + lane);
+      const int ps = piece_slot();
+      if (!ok) break;
+      tree_publish(a, pc, k, lane, info[ps]);
+      const int rows = pc.nodes * G;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&piece_full[ps], rows * D * 2);
+        if (pc.p1 <= pc.live) mbar_arrive(&draft_go[ps]);  // no draft page in this piece
+      }
+      __syncwarp();
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
+      for (int r = lane; r < rows; r += 32)
+        bulk_g2s(qbuf + (ps * C::kRows + r) * C::kQPitch,
+                 q + ((int64_t(pc.hd.b) * a.T + pc.node0 + r / G) * a.num_q_heads + pc.hd.kv * G + r % G) * D, D * 2,
+                 &piece_full[ps]);
+      ++pi;
+      for (int p = pc.p0; p < pc.p1; ++p, ++k) {
         const int i = (p - pc.p0) & 31;
-        if (i == 0 && p + lane < pc.live) mine = *reinterpret_cast<const int4*>(rec + p + lane);
+        if (i == 0 && p > pc.p0 && p + lane < pc.live) mine = *reinterpret_cast<const int4*>(rec + p + lane);
         PageDesc pg;
-        pg.phys = __shfl_sync(0xffffffffu, mine.x, i);
-        pg.abs_start = __shfl_sync(0xffffffffu, mine.y, i);
-        pg.span = __shfl_sync(0xffffffffu, mine.z, i);
+        pg.phys = __shfl_sync(kAll, mine.x, i);
+        pg.abs_start = __shfl_sync(kAll, mine.y, i);
+        pg.span = __shfl_sync(kAll, mine.z, i);
         pg.head = pc.head;
         const int s = k % NST;
-        ok = k < NST || __shfl_sync(0xffffffffu, int(lane == 0 && mbar_wait(&empty[s], ((k / NST) & 1) ^ 1)), 0);
+        ok = k < NST || __shfl_sync(kAll, int(lane == 0 && mbar_wait(&empty[s], ((k / NST) & 1) ^ 1)), 0);
         if (!ok) {
           if (lane == 0) record_error(a.status, kDevTimeoutEmpty);
           break;
         }
         uint8_t* kd = stage + s * 2 * PB;
-        if (p >= pc.live) {  // the draft's page
-          tree_draft_page<D, FP8>(a, pc.hd, pc.n, kd, P * 128, kd + PB, lane);
-          fence_proxy_async_smem();  // before a later bulk copy into this stage
-          __syncwarp();
+        if (p >= pc.live) {  // the draft's page: its writers arrive when they have filled it
           if (lane == 0) {
             sdesc[s] = PageDesc{kDraftPage, 0, 0, pc.head};
             mbar_arrive(&full[s]);
+            mbar_arrive(&draft_go[ps]);  // the stage is free
           }
-        } else if (lane == 0) {
+          continue;
+        }
+        if (lane == 0) {
           if (slot_hi(pg) > slot_lo(pg) && (pg.phys < 0 || pg.phys >= a.pool_pages)) {
             record_error(a.status, kDevBadPage);  // corrupted table: report, read nothing
             pg.span = 0;
@@ -112,12 +154,52 @@ __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 
           } else {
             mbar_arrive(&full[s]);  // an empty record: nothing to read
           }
+#pragma unroll
+          for (int w = 0; w < ND; ++w) mbar_arrive(&full[s]);
         }
       }
     }
-    if (lane == 0)  // never leave with copies in flight
+    // never leave with copies in flight
+    const int last = pi;
+    if (ok) {
+      const int ps = piece_slot();
+      if (ok && lane == 0) {
+        info[ps].pc.head = -1;
+        mbar_arrive(&piece_full[ps]);
+      }
+    }
+    if (lane == 0) {
+      // Q rows: the end mark took the slot of the last piece but one, after its readers
+      for (int j = max(0, last - (ok ? 1 : 2)); j < last; ++j)
+        if (!mbar_wait(&piece_full[j & 1], (j >> 1) & 1)) break;
       for (int j = (k > NST ? k - NST : 0); j < k; ++j)
         if (!mbar_wait(&full[j % NST], (j / NST) & 1)) break;
+    }
+    return;
+  }
+
+  if (warp > NC) {
+    // ------------------------------ draft page ------------------------------
+    const bool does_k = warp == NC + 1, does_v = warp == NC + ND;
+    for (int pi = 0;; ++pi) {
+      const int ps = pi & 1;
+      if (!__all_sync(kAll, mbar_wait(&piece_full[ps], (pi >> 1) & 1))) break;
+      const Info& in = info[ps];
+      if (in.pc.head < 0) break;
+      if (in.pc.p1 > in.pc.live) {
+        const int kd = in.stage0 + in.pc.p1 - 1 - in.pc.p0, s = kd % NST;
+        // the producer has seen the stage free (a wait on the stage's own barrier could be phases ahead of it)
+        if (!__all_sync(kAll, mbar_wait(&draft_go[ps], (pi >> 1) & 1))) break;
+        uint8_t* page = stage + s * 2 * PB;
+        if (does_k) tree_draft_k<D, FP8>(a, in.pc.hd, in.pc.n, page, P * 128, lane);
+        if (does_v) tree_draft_v<D, FP8>(a, in.pc.hd, in.pc.n, page + PB, lane);
+        fence_proxy_async_smem();  // before a later bulk copy into this stage
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[s]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&piece_free[ps]);
+    }
     return;
   }
 
@@ -125,35 +207,39 @@ __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 
   auto bar = [] { asm volatile("bar.sync 1, %0;" ::"n"(NC * 32) : "memory"); };
   const int wr = warp / WT, wt = warp % WT;
   const int grp = lane >> 2, tq = lane & 3, mi = lane >> 3, rr = lane & 7;
-  const int G = a.group;
   const int row[2] = {wr * 16 + grp, wr * 16 + grp + 8};
   bool ok = true;
-  while (split.next(a, walk, pc)) {
+  for (int pi = 0;; ++pi) {
+    const int ps = pi & 1;
+    // all consumers go on, or none (a barrier waits for every one of them); also: the previous piece's buffers are read
+    const bool got = ok && __all_sync(kAll, mbar_wait(&piece_full[ps], (pi >> 1) & 1));
+    if (ok && !got) record_error(a.status, kDevTimeoutFull);
+    if (!bar_red_and(1, NC * 32, got)) break;
+    const Info& in = info[ps];
+    if (in.pc.head < 0) break;
+    const typename Split::Piece pc = in.pc;
     uint64_t nodes[2];
-    tree_ancestors(a, pc.hd.b, pc.n, lane, nodes);
+    tree_ancestors(in.up[lane], in.up[lane + 32], lane, nodes);
     const int rows = pc.nodes * G;
     const int p_last = pc.hd.ctx_len + pc.n - 1;
     int pos[2] = {0, 0};
     uint64_t anc[2] = {0, 0};
     uint32_t qa[KSTEPS][4];
-    const __nv_bfloat16* qrow[2];
+    const uint8_t* qrow[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      qrow[x] = nullptr;
       const uint64_t mask = tree_mask_of(nodes, min(pc.node0 + row[x] / G, kMaxTreeNodes - 1));
       if (row[x] < rows) {
         anc[x] = tree_visible(mask, pc.hd);
         pos[x] = pc.hd.ctx_len + __popcll(mask) - 1;
-        qrow[x] = static_cast<const __nv_bfloat16*>(a.q) +
-                  ((int64_t(pc.hd.b) * a.T + pc.node0 + row[x] / G) * a.num_q_heads + pc.hd.kv * G + row[x] % G) * D;
       }
+      qrow[x] = qbuf + (ps * C::kRows + row[x]) * C::kQPitch;  // rows behind the last hold anything: never written out
     }
     if constexpr (FP8) {  // k-steps 2j, 2j+1 cover dims 32j .. 32j+31 in the K loads' order
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {
-        const int c0 = j * 32 + tq * 8;
-        const uint4 x0 = qrow[0] ? *reinterpret_cast<const uint4*>(qrow[0] + c0) : make_uint4(0, 0, 0, 0);
-        const uint4 x1 = qrow[1] ? *reinterpret_cast<const uint4*>(qrow[1] + c0) : make_uint4(0, 0, 0, 0);
+        const uint4 x0 = *reinterpret_cast<const uint4*>(qrow[0] + (j * 32 + tq * 8) * 2);
+        const uint4 x1 = *reinterpret_cast<const uint4*>(qrow[1] + (j * 32 + tq * 8) * 2);
         qa[2 * j][0] = bf16x2_to_f16x2(x0.x), qa[2 * j][2] = bf16x2_to_f16x2(x0.y);
         qa[2 * j + 1][0] = bf16x2_to_f16x2(x0.z), qa[2 * j + 1][2] = bf16x2_to_f16x2(x0.w);
         qa[2 * j][1] = bf16x2_to_f16x2(x1.x), qa[2 * j][3] = bf16x2_to_f16x2(x1.y);
@@ -164,8 +250,8 @@ __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 
       for (int kk = 0; kk < KSTEPS; ++kk)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          qa[kk][x] = qrow[x] ? *reinterpret_cast<const uint32_t*>(qrow[x] + kk * 16 + tq * 2) : 0u;
-          qa[kk][x + 2] = qrow[x] ? *reinterpret_cast<const uint32_t*>(qrow[x] + kk * 16 + tq * 2 + 8) : 0u;
+          qa[kk][x] = *reinterpret_cast<const uint32_t*>(qrow[x] + (kk * 16 + tq * 2) * 2);
+          qa[kk][x + 2] = *reinterpret_cast<const uint32_t*>(qrow[x] + (kk * 16 + tq * 2 + 8) * 2);
         }
     }
     float o[NT][4];
@@ -287,7 +373,6 @@ __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 
       l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
     }
     if constexpr (WT > 1) {
-      bar();  // the previous piece's buffers are read
       if (wt > 0) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -347,7 +432,7 @@ __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 
         } else {
 #pragma unroll
           for (int j = 0; j < NT; ++j)
-            *reinterpret_cast<float2*>(slot + row[x] * D + j * 8 + tq * 2) =
+            *reinterpret_cast<float2*>(slot + tree_acc_at(row[x], j * 8 + tq * 2, rows_max)) =
                 make_float2(o[j][2 * x], o[j][2 * x + 1]);
           if (tq == 0)
             *reinterpret_cast<float2*>(slot + rows_max * D + 2 * row[x]) = make_float2(m[x], l[x]);
@@ -355,6 +440,8 @@ __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 
       }
     }
     if (threadIdx.x == 0) tree_note_join(a, pc);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&piece_free[ps]);
   }
 }
 
@@ -390,7 +477,7 @@ __global__ void __launch_bounds__(kF32Threads) tree_f32_kernel(TreeLaunch a) {
     auto at_row = [&](int r) { return (q0 + r / G) * a.num_q_heads + pc.hd.kv * G + r % G; };
     if (tid < 32) {  // one warp holds all rows' nodes
       uint64_t nodes[2];
-      tree_ancestors(a, pc.hd.b, pc.n, tid, nodes);
+      tree_ancestors(tree_parent(a, pc.hd.b, pc.n, tid), tree_parent(a, pc.hd.b, pc.n, tid + 32), tid, nodes);
       const uint64_t mask = tree_mask_of(nodes, min(pc.node0 + tid / G, kMaxTreeNodes - 1));
       if (tid < rows) {
         anc[tid] = tree_visible(mask, pc.hd);
@@ -478,7 +565,7 @@ __global__ void __launch_bounds__(kF32Threads) tree_f32_kernel(TreeLaunch a) {
         if (col == 0 && a.lse) a.lse[at_row(r)] = (M + log2f(L)) * kTreeLn2;
       } else {
         float* slot = a.partial + int64_t(pc.slot) * tree_slot_floats(a);
-        slot[r * D + col] = acc[j];
+        slot[tree_acc_at(r, col, rows_max)] = acc[j];
         if (col == 0) slot[rows_max * D + 2 * r] = M, slot[rows_max * D + 2 * r + 1] = L;
       }
     }

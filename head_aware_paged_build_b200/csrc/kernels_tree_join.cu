@@ -2,16 +2,17 @@
 //
 // With m_i, l_i, acc_i the running maximum (log2 domain), sum and unnormalised
 // output of piece i:  M = max m_i,  O = sum 2^(m_i - M) acc_i / sum 2^(m_i - M) l_i,
-// pieces in line order, so the same inputs give the same bits.
+// in an order that the pieces' numbers fix, so the same inputs give the same bits.
 //
 // A programmatic dependent launch: its blocks are placed while the attention's
 // last CTAs run and wait for that grid on the device.  (The last CTA of a row
 // group joining it instead was 3 to 10 times slower on the 8K and 32K layers:
 // one SM reads what a dozen wrote, 64 KB for each piece of 128 rows.)  Every
-// block lists the split groups (the CTA a group starts in left its description),
-// and they share out the rows: eight rows an item, a warp each, or two rows an
-// item, four warps each, when there are few rows and so probably many pieces.
-// Bound by L2 latency: a warp keeps eight pieces' loads in flight.
+// block lists the split groups (the CTA a group starts in left its description)
+// and takes its share of items.  A thread holds a row's 16 columns over a part
+// of the pieces; a group of many pieces is divided into 4 or 16 parts, which
+// meet in shared memory.  Bound by L2 latency: a thread asks for kBatch pieces
+// (maximum, sum and columns) at once and rescales once a batch.
 #include "kernels.h"
 #include "tree_common.cuh"
 
@@ -19,33 +20,33 @@ namespace sp {
 namespace {
 
 constexpr int kJoinThreads = 256;
-constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kBatch = 4;
+constexpr int kCols = 16;
+
+// Parts a group's pieces are divided into: one while a batch holds them.
+__device__ __forceinline__ int join_parts(int n_pieces) {
+  return n_pieces <= kBatch ? 1 : n_pieces <= 4 * kBatch ? 4 : 16;
+}
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeLaunch a) {
-  constexpr int V = D / 32;  // columns of a lane
+  constexpr int CG = D / kCols;           // column groups of a row
+  constexpr int R1 = kJoinThreads / CG;   // rows of an item in one part
+  constexpr int PER = kTreeMaxCtas / 32;
   __shared__ int s_end[kTreeMaxCtas];  // items up to and with each CTA's group
-  __shared__ float s_acc[kJoinWarps][D];
-  __shared__ float s_l[kJoinWarps];
-  __shared__ int s_few;
+  __shared__ float s_part[kJoinThreads][kCols + 1];
+  __shared__ float2 s_ml[kJoinThreads];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int c = threadIdx.x; c < a.n_ctas; c += kJoinThreads)
-    s_end[c] = a.joins[c].n_pieces > 0 ? a.joins[c].rows : 0;
+  const int tid = threadIdx.x, lane = tid & 31;
+  for (int c = tid; c < a.n_ctas; c += kJoinThreads) {
+    const int n = a.joins[c].n_pieces, per = R1 / join_parts(n);
+    s_end[c] = n > 0 ? (a.joins[c].rows + per - 1) / per : 0;
+  }
   __syncthreads();
-  if (warp == 0) {
-    constexpr int PER = kTreeMaxCtas / 32;
-    int rows = 0;
-    for (int i = 0; i < PER; ++i) rows += lane * PER + i < a.n_ctas ? s_end[lane * PER + i] : 0;
-    const int all = __reduce_add_sync(0xffffffffu, rows);
-    const bool few = all <= 4 * int(gridDim.x);
-    const int per = few ? 2 : kJoinWarps;
+  if (tid < 32) {
     int items = 0;
     for (int i = 0; i < PER; ++i)
-      if (lane * PER + i < a.n_ctas) {
-        items += (s_end[lane * PER + i] + per - 1) / per;
-        s_end[lane * PER + i] = items;
-      }
+      if (lane * PER + i < a.n_ctas) s_end[lane * PER + i] = items += s_end[lane * PER + i];
     int upto = items;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -54,10 +55,8 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeLaunch a) {
     }
     for (int i = 0; i < PER; ++i)
       if (lane * PER + i < a.n_ctas) s_end[lane * PER + i] += upto - items;
-    if (lane == 0) s_few = few;
   }
   __syncthreads();
-  const bool few = s_few;
   const int rows_max = a.nodes_per_group * a.group;
   const int64_t stride = tree_slot_floats(a);
   const int total = s_end[a.n_ctas - 1];
@@ -69,80 +68,104 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeLaunch a) {
       else lo = mid + 1;
     }
     const TreeJoin jn = a.joins[lo];
-    const int in_group = item - (lo ? s_end[lo - 1] : 0);
-    const int W = few ? 4 : 1;  // warps a row
-    const int row = few ? in_group * 2 + warp / 4 : in_group * kJoinWarps + warp, part = few ? warp % 4 : 0;
-    auto slot = [&](int i) { return a.partial + int64_t(i == 0 ? jn.first_slot : 2 * (lo + i)) * stride; };
-    float M = -INFINITY, l = 0.f, acc[V];
+    const int parts = join_parts(jn.n_pieces), R = R1 / parts;
+    const int row0 = (item - (lo ? s_end[lo - 1] : 0)) * R;
+    // thread = (part, column group, row of the item)
+    const int row = row0 + tid % R, cg = tid / R % CG, part = tid / (R * CG);
+    float m = -INFINITY, l = 0.f, acc[kCols];
 #pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = 0.f;
+    for (int e = 0; e < kCols; ++e) acc[e] = 0.f;
     if (row < jn.rows) {
-      for (int i = lane; i < jn.n_pieces; i += 32) M = fmaxf(M, __ldcg(slot(i) + rows_max * D + 2 * row));
+      for (int i0 = part; i0 < jn.n_pieces; i0 += kBatch * parts) {
+        float2 ml[kBatch];
+        float4 x[kBatch][kCols / 4];
+        float top = m;
 #pragma unroll
-      for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      const float base = M == -INFINITY ? 0.f : M;
-      constexpr int B = 8;  // pieces in flight
-      for (int i0 = part; i0 < jn.n_pieces; i0 += B * W) {
-        float2 ml[B];
-        float x[B][V];
-#pragma unroll
-        for (int u = 0; u < B; ++u) {
-          const int i = i0 + u * W;
+        for (int u = 0; u < kBatch; ++u) {
+          const int i = i0 + u * parts;
           ml[u] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-          for (int v = 0; v < V; ++v) x[u][v] = 0.f;
           if (i >= jn.n_pieces) continue;
-          const float* s = slot(i);
+          const float* s = a.partial + int64_t(i == 0 ? jn.first_slot : 2 * (lo + i)) * stride;
           ml[u] = __ldcg(reinterpret_cast<const float2*>(s + rows_max * D + 2 * row));
-          if constexpr (V == 4)
-            *reinterpret_cast<float4*>(x[u]) = __ldcg(reinterpret_cast<const float4*>(s + row * D + lane * V));
-          else
-            *reinterpret_cast<float2*>(x[u]) = __ldcg(reinterpret_cast<const float2*>(s + row * D + lane * V));
+#pragma unroll
+          for (int c = 0; c < kCols / 4; ++c)
+            x[u][c] = __ldcg(reinterpret_cast<const float4*>(s + tree_acc_at(row, cg * kCols + 4 * c, rows_max)));
         }
 #pragma unroll
-        for (int u = 0; u < B; ++u) {
+        for (int u = 0; u < kBatch; ++u) top = fmaxf(top, ml[u].x);
+        const float base = top == -INFINITY ? 0.f : top, f0 = exp2f(m - base);
+        m = top;
+        l *= f0;
+#pragma unroll
+        for (int e = 0; e < kCols; ++e) acc[e] *= f0;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          if (i0 + u * parts >= jn.n_pieces) continue;
           const float f = exp2f(ml[u].x - base);
           l += f * ml[u].y;
 #pragma unroll
-          for (int v = 0; v < V; ++v) acc[v] += f * x[u][v];
+          for (int c = 0; c < kCols / 4; ++c) {
+            acc[4 * c] += f * x[u][c].x, acc[4 * c + 1] += f * x[u][c].y;
+            acc[4 * c + 2] += f * x[u][c].z, acc[4 * c + 3] += f * x[u][c].w;
+          }
         }
       }
     }
-    if (few) {  // the row's four warps, in order
-      __syncthreads();
+    auto out_row = [&](int r) {
+      return (int64_t(jn.b) * a.T + jn.node0 + r / a.group) * a.num_q_heads + jn.kv * a.group + r % a.group;
+    };
+    if (parts == 1) {
+      if (row >= jn.rows) continue;
+      const int64_t at = out_row(row);
+      const float inv = a.v_scale / l;
+      T* dst = static_cast<T*>(a.out) + at * D + cg * kCols;
+      if constexpr (sizeof(T) == 2) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) s_acc[warp][lane * V + v] = acc[v];
-      if (lane == 0) s_l[warp] = l;
-      __syncthreads();
-      if (part != 0) continue;
+        for (int e = 0; e < kCols; e += 8)
+          reinterpret_cast<uint4*>(dst)[e / 8] = make_uint4(
+              pack_bf16x2(acc[e] * inv, acc[e + 1] * inv), pack_bf16x2(acc[e + 2] * inv, acc[e + 3] * inv),
+              pack_bf16x2(acc[e + 4] * inv, acc[e + 5] * inv), pack_bf16x2(acc[e + 6] * inv, acc[e + 7] * inv));
+      } else {
 #pragma unroll
-      for (int w = 1; w < 4; ++w) {
-        l += s_l[warp + w];
-#pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] += s_acc[warp + w][lane * V + v];
+        for (int e = 0; e < kCols; e += 4)
+          reinterpret_cast<float4*>(dst)[e / 4] =
+              make_float4(acc[e] * inv, acc[e + 1] * inv, acc[e + 2] * inv, acc[e + 3] * inv);
       }
+      if (cg == 0 && a.lse) a.lse[at] = (m + log2f(l)) * kTreeLn2;
+      continue;
     }
-    if (row >= jn.rows) continue;
-    const int64_t at =
-        (int64_t(jn.b) * a.T + jn.node0 + row / a.group) * a.num_q_heads + jn.kv * a.group + row % a.group;
-    const float inv = a.v_scale / l;
-    T* dst = static_cast<T*>(a.out) + at * D + lane * V;
-    if constexpr (sizeof(T) == 2) {
+    // the parts meet, in order: a thread takes single columns
+    __syncthreads();  // the previous item's sums are read
 #pragma unroll
-      for (int v = 0; v < V; v += 2)
-        reinterpret_cast<uint32_t*>(dst)[v / 2] = pack_bf16x2(acc[v] * inv, acc[v + 1] * inv);
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; ++v) dst[v] = acc[v] * inv;
+    for (int e = 0; e < kCols; ++e) s_part[tid][e] = acc[e];
+    s_ml[tid] = make_float2(m, l);
+    __syncthreads();
+    for (int e = tid; e < R * D; e += kJoinThreads) {
+      const int r = e / D, col = e % D, at0 = col / kCols * R + r;  // the thread of part 0
+      if (row0 + r >= jn.rows) continue;
+      float M = -INFINITY;
+      for (int p = 0; p < parts; ++p) M = fmaxf(M, s_ml[p * R * CG + at0].x);
+      const float base = M == -INFINITY ? 0.f : M;
+      float L = 0.f, x = 0.f;
+      for (int p = 0; p < parts; ++p) {
+        const float2 ml = s_ml[p * R * CG + at0];
+        const float f = exp2f(ml.x - base);
+        L += f * ml.y;
+        x += f * s_part[p * R * CG + at0][col % kCols];
+      }
+      const int64_t at = out_row(row0 + r);
+      x *= a.v_scale / L;
+      if constexpr (sizeof(T) == 2) static_cast<__nv_bfloat16*>(a.out)[at * D + col] = __float2bfloat16_rn(x);
+      else static_cast<float*>(a.out)[at * D + col] = x;
+      if (col == 0 && a.lse) a.lse[at] = (M + log2f(L)) * kTreeLn2;
     }
-    if (lane == 0 && a.lse) a.lse[at] = (M + log2f(l)) * kTreeLn2;
   }
 }
 
 template <typename T, int D>
 cudaError_t launch(const TreeLaunch& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(4 * 148);
+  cfg.gridDim = dim3(2 * 148);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];

@@ -15,12 +15,13 @@
 // 1.5 us of an SM's share, its two products 0.75 us); two tiles a CTA double the
 // products on the same bytes.
 //
-// Warp roles (384 threads; warps 2 and 3 only make up the first warpgroup, whose
-// spare registers go to the softmax threads):
-//   warp 0     producer: Q tiles by TMA (128-byte swizzle), K and V pages by bulk
-//              copies into a ring of stages (pool pages are stored as the tensor
-//              cores' operands), the draft's rows as one more page it writes itself
+// Warp roles (384 threads; the first warpgroup's spare registers go to the
+// softmax threads):
+//   warp 0     producer: walks the CTA's pieces and hands each to the others a slot
+//              ahead; Q tiles by TMA (128-byte swizzle), K and V pages by bulk copies
+//              into a ring of stages (pool pages are stored as the tensor cores' operands)
 //   warp 1     TMEM owner and MMA issuer (one thread)
+//   warps 2, 3 the draft's K and V rows, written as one more page of a stage
 //   warps 4-7  softmax of stream 0, warps 8-11 of stream 1: a thread a row, the
 //              whole 128-score row in registers; lazy rescale of O (only when the
 //              row's maximum grows by more than 2^8), P written as bf16 over S
@@ -60,26 +61,33 @@ struct TreeTc {
   static constexpr int kOffStage = kQTiles * kQ;
   static constexpr int kOffMl = kOffStage + NS * kStage;  // (m, l) of each row and stream
   static constexpr int kOffDesc = kOffMl + 2 * 128 * 8;
-  static constexpr int kOffScan = kOffDesc + NS * 2 * 16;
-  static constexpr int kOffBar = kOffScan + (kThreads / 32 + 2) * 8;
-  static constexpr int kBytes = kOffBar + (8 + 2 * NS) * 8 + 16;
+  static constexpr int kOffInfo = kOffDesc + NS * 2 * 16;
+  using Split = TreeSplit<2, 2, 3>;
+  using Info = TreePieceInfo<typename Split::Piece>;
+  static constexpr int kOffBar = kOffInfo + (2 * int(sizeof(Info)) + 7) / 8 * 8;
+  static constexpr int kBytes = kOffBar + (14 + 2 * NS) * 8 + 8;
   static_assert(kBytes <= 232448, "shared memory of a CTA");
-  using Split = TreeSplit<2, 2, 4>;
+  static_assert(kOffStage % 1024 == 0 && kStage % 1024 == 0 && kOffMl % 8 == 0 && kOffDesc % 16 == 0 &&
+                    kOffInfo % alignof(Info) == 0 && kOffBar % 8 == 0,
+                "alignment of the shared-memory parts");
+  static_assert((kThreads / 32 + 2) * 8 <= 2 * 128 * 8, "the split's scratch lies in the statistics' place");
 };
 
 template <int D, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, TreeLaunch a) {
   using C = TreeTc<D, WIDE>;
   using Split = typename C::Split;
+  using Info = typename C::Info;
   constexpr int NS = C::NS;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* stage_s = smem + C::kOffStage;
   float2* ml_s = reinterpret_cast<float2*>(smem + C::kOffMl);
   PageDesc* sdesc = reinterpret_cast<PageDesc*>(smem + C::kOffDesc);
-  int64_t* scratch = reinterpret_cast<int64_t*>(smem + C::kOffScan);
+  Info* info = reinterpret_cast<Info*>(smem + C::kOffInfo);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t *q_full = bars, *q_free = bars + 1, *o_done = bars + 2, *done = bars + 3;
-  uint64_t *s_full = bars + 4, *p_full = bars + 6, *kv_full = bars + 8, *kv_free = kv_full + NS;
+  uint64_t *s_full = bars + 4, *p_full = bars + 6, *piece_full = bars + 8, *piece_free = bars + 10;
+  uint64_t *draft_go = bars + 12, *kv_full = bars + 14, *kv_free = kv_full + NS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(kv_free + NS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -92,9 +100,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     for (int x = 0; x < 2; ++x) {
       mbar_init(&s_full[x], 1);
       mbar_init(&p_full[x], 128);
+      mbar_init(&piece_full[x], 1);
+      mbar_init(&draft_go[x], 1);
+      mbar_init(&piece_free[x], 8 + 1 + 2);  // softmax warps, MMA issuer, draft warps
     }
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&kv_full[s], 1);
+      mbar_init(&kv_full[s], 3);  // the producer and the draft's two writers (without a draft it arrives for them)
       mbar_init(&kv_free[s], 1);
     }
     *abort_flag = 0;
@@ -102,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     tc::prefetch_tensormap(&qmap);
   }
   Split split;
-  if (!split.template init<kThreads>(a, scratch)) return;
+  if (!split.template init<kThreads>(a, reinterpret_cast<int64_t*>(ml_s))) return;
   if (warp == 1) {
     tc::tmem_alloc(tmem_slot, kTmemCols);
     tc::tmem_relinquish();
@@ -119,8 +130,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     *abort_flag = 1;
   };
   const int G = a.group, npt = a.nodes_per_tile;
-  typename Split::Walk walk = split.walk();
-  typename Split::Piece pc;
   int k = 0;   // KV tiles of the earlier pieces
   int pi = 0;  // pieces so far
   bool ok = true;
@@ -131,29 +140,44 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
       // ------------------------------ producer ------------------------------
       const uint8_t* kpool = static_cast<const uint8_t*>(a.kpool);
       const uint8_t* vpool = static_cast<const uint8_t*>(a.vpool);
+      typename Split::Walk walk = split.walk();
+      typename Split::Piece pc;
+      auto piece_slot = [&] {  // the next piece's slot, once it is free
+        const int ps = pi & 1;
+        ok = pi < 2 || __shfl_sync(kAll, int(lane == 0 && mbar_wait(&piece_free[ps], ((pi >> 1) - 1) & 1)), 0);
+        if (!ok && lane == 0) fail(kDevTimeoutEmpty);
+        return ps;
+      };
       while (ok && split.next(a, walk, pc)) {
         const bool two = WIDE && pc.nodes > npt;
-        if (lane == 0) {
-          ok = pi == 0 || mbar_wait(q_free, (pi - 1) & 1);
-          if (ok) {
-            mbar_arrive_expect_tx(q_full, (two ? 2 : 1) * (D / 64) * npt * G * 128);
-            for (int x = 0; x < (two ? 2 : 1); ++x)
-#pragma unroll
-              for (int h = 0; h < D / 64; ++h)
-                tc::tma_load_3d(smem + x * C::kQ + h * 16384, &qmap, h * 64, pc.hd.kv * G,
-                                pc.hd.b * a.T + pc.node0 + x * npt, q_full);
-          }
-        }
-        ok = __shfl_sync(kAll, int(ok), 0);
-        if (!ok) {
-          if (lane == 0) fail(kDevTimeoutMma);
-          break;
-        }
-        ++pi;
         const PageDesc* rec = a.pages + pc.hd.vpage_begin;
         int4 mine = make_int4(0, 0, 0, 0);
+        if (pc.p0 + lane < pc.live) mine = *reinterpret_cast<const int4*>(rec + pc.p0 + lane);
+        const int ps = piece_slot();
+        if (!ok) break;
+        tree_publish(a, pc, k, lane, info[ps]);
+        if (lane == 0) {
+          mbar_arrive(&piece_full[ps]);
+          if (pc.p1 <= pc.live) mbar_arrive(&draft_go[ps]);  // no draft page in this piece
+        }
+        auto load_q = [&] {  // behind the first KV tiles: its place is free only after the previous piece's last S
+          if (lane == 0) {
+            ok = pi == 0 || mbar_wait(q_free, (pi - 1) & 1);
+            if (ok) {
+              mbar_arrive_expect_tx(q_full, (two ? 2 : 1) * (D / 64) * npt * G * 128);
+              for (int x = 0; x < (two ? 2 : 1); ++x)
+#pragma unroll
+                for (int h = 0; h < D / 64; ++h)
+                  tc::tma_load_3d(smem + x * C::kQ + h * 16384, &qmap, h * 64, pc.hd.kv * G,
+                                  pc.hd.b * a.T + pc.node0 + x * npt, q_full);
+            } else {
+              fail(kDevTimeoutMma);
+            }
+          }
+          ok = __shfl_sync(kAll, int(ok), 0);
+        };
         const int nt = (pc.p1 - pc.p0 + 1) / 2;
-        for (int j = 0; j < nt; ++j, ++k) {
+        for (int j = 0; ok && j < nt; ++j, ++k) {
           const int st = k % NS;
           uint8_t* k_s = stage_s + st * C::kStage;
           uint8_t* v_s = k_s + C::kK;
@@ -161,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int p = pc.p0 + 2 * j + h, i = (2 * j + h) & 31;
-            if (i == 0 && p + lane < pc.live) mine = *reinterpret_cast<const int4*>(rec + p + lane);
+            if (i == 0 && p > pc.p0 && p + lane < pc.live) mine = *reinterpret_cast<const int4*>(rec + p + lane);
             pg[h] = PageDesc{__shfl_sync(kAll, mine.x, i), __shfl_sync(kAll, mine.y, i), __shfl_sync(kAll, mine.z, i),
                              0};
             if (p >= pc.live) pg[h] = PageDesc{p == pc.live && p < pc.p1 ? kDraftPage : kNoPage, 0, 0, 0};
@@ -177,17 +201,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
             break;
           }
           int bytes = 0;
+          bool draft = false;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (pg[h].phys >= 0) {
-              bytes += (C::kK + C::kV) / 2;
-            } else {
-              if (pg[h].phys == kDraftPage) {
-                tree_draft_page<D, false>(a, pc.hd, pc.n, k_s + h * 8192, 16384, v_s + h * (D * 128), lane);
-              } else {  // no page: weights of zero meet values of zero
-                for (int e = lane; e < D * 8; e += 32)
-                  reinterpret_cast<uint4*>(v_s + h * (D * 128))[e] = make_uint4(0, 0, 0, 0);
-              }
+            if (pg[h].phys >= 0) bytes += (C::kK + C::kV) / 2;
+            else if (pg[h].phys == kDraftPage) draft = true;
+            else {  // no page: weights of zero meet values of zero
+              for (int e = lane; e < D * 8; e += 32)
+                reinterpret_cast<uint4*>(v_s + h * (D * 128))[e] = make_uint4(0, 0, 0, 0);
               fence_proxy_async_smem();
             }
           }
@@ -204,8 +225,21 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
                 bulk_g2s(k_s + c * 16384 + h * 8192, kpool + off + c * 8192, 8192, &kv_full[st]);
               bulk_g2s(v_s + h * (D * 128), vpool + off, D * 128, &kv_full[st]);
             }
+            if (draft) mbar_arrive(&draft_go[ps]);  // the stage is free
+            else mbar_arrive(&kv_full[st]), mbar_arrive(&kv_full[st]);
           }
           __syncwarp();
+          if (j == min(1, nt - 1)) {
+            load_q();
+            if (ok) ++pi;
+          }
+        }
+      }
+      if (ok) {
+        const int ps = piece_slot();
+        if (ok && lane == 0) {
+          info[ps].pc.head = -1;
+          mbar_arrive(&piece_full[ps]);
         }
       }
       // drain: never leave with copies still writing this CTA's shared memory
@@ -243,9 +277,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
             tc::mma_bf16_ts(t_o(x), t_s(x) + kk * 8, vd + (((kk >> 2) * (D * 128) + (kk & 3) * 32) >> 4), idesc_o,
                             (acc || kk > 0) ? 1u : 0u);
         };
-        while (ok && split.next(a, walk, pc)) {
-          const bool two = WIDE && pc.nodes > npt;
-          const int nt = (pc.p1 - pc.p0 + 1) / 2, U = two ? 2 * nt : nt;
+        while (ok) {
+          const int ps = pi & 1;
+          if (!mbar_wait(&piece_full[ps], (pi >> 1) & 1)) {
+            fail(kDevTimeoutFull);
+            break;
+          }
+          if (info[ps].pc.head < 0) break;
+          const bool two = WIDE && info[ps].pc.nodes > npt;
+          const int nt = (info[ps].pc.p1 - info[ps].pc.p0 + 1) / 2, U = two ? 2 * nt : nt;
+          mbar_arrive(&piece_free[ps]);
           auto tile_of = [&](int u) { return k + (two ? u >> 1 : u); };
           if (!mbar_wait(q_full, pi & 1)) {
             fail(kDevTimeoutFull);
@@ -286,6 +327,27 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         mbar_wait(done, 0);
       }
       __syncwarp();
+    } else {
+      // ------------------------------ draft page ------------------------------
+      for (;; ++pi) {
+        const int ps = pi & 1;
+        if (!__all_sync(kAll, mbar_wait(&piece_full[ps], (pi >> 1) & 1))) break;
+        const Info& in = info[ps];
+        if (in.pc.head < 0) break;
+        if (in.pc.p1 > in.pc.live) {
+          const int at = in.pc.p1 - 1 - in.pc.p0, tile = in.stage0 + at / 2, h = at & 1, st = tile % NS;
+          // the producer has seen the stage free (a wait on the stage's own barrier could be phases ahead of it)
+          if (!__all_sync(kAll, mbar_wait(&draft_go[ps], (pi >> 1) & 1))) break;
+          uint8_t* k_s = stage_s + st * C::kStage;
+          if (warp == 2) tree_draft_k<D, false>(a, in.pc.hd, in.pc.n, k_s + h * 8192, 16384, lane);
+          else tree_draft_v<D, false>(a, in.pc.hd, in.pc.n, k_s + C::kK + h * (D * 128), lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&kv_full[st]);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&piece_free[ps]);
+      }
     }
   } else {
     tc::reg_alloc<kRegsSoftmax>();
@@ -298,14 +360,21 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     const float sl2 = a.scale_log2;
     uint32_t turn = 0;  // tiles of this stream so far
     auto bar = [] { asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory"); };
-    while (split.next(a, walk, pc)) {
+    for (;; ++pi) {
+      const int ps = pi & 1;
+      // all softmax warps go on, or none: the barriers wait for every one of them
+      const bool got = ok && __all_sync(kAll, mbar_wait(&piece_full[ps], (pi >> 1) & 1));
+      if (ok && !got) fail(kDevTimeoutFull);
+      if (!bar_red_and(1, kSoftmaxThreads, got)) break;
+      if (info[ps].pc.head < 0) break;
+      const typename Split::Piece pc = info[ps].pc;
       const bool two = WIDE && pc.nodes > npt;
       const int nt = (pc.p1 - pc.p0 + 1) / 2, U = two ? 2 * nt : nt;
       const int first_node = pc.node0 + (two ? x * npt : 0);
       const int rows = min(npt, pc.node0 + pc.nodes - first_node) * G;
       const bool busy = quarter * 32 < rows;  // any row in this warp
       uint64_t nodes[2];
-      tree_ancestors(a, pc.hd.b, pc.n, lane, nodes);
+      tree_ancestors(info[ps].up[lane], info[ps].up[lane + 32], lane, nodes);
       const uint64_t mask = tree_mask_of(nodes, min(first_node + r / G, kMaxTreeNodes - 1));
       const uint64_t anc = tree_visible(mask, pc.hd);
       const int pos = pc.hd.ctx_len + __popcll(mask) - 1;
@@ -314,7 +383,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
       for (int u = x; u < U; u += 2, ++turn) {
         const int tile = k + (two ? u >> 1 : u), st = tile % NS;
         // waits are voted: tcgen05.ld / st need the whole warp
-        if (ok && !__all_sync(kAll, mbar_wait(&kv_full[st], (tile / NS) & 1) && mbar_wait(&s_full[x], turn & 1))) {
+        // (S_x first: then the stage's phase is this tile's, and its descriptors are read behind that barrier too)
+        if (ok && !__all_sync(kAll, mbar_wait(&s_full[x], turn & 1) && mbar_wait(&kv_full[st], (tile / NS) & 1))) {
           fail(kDevTimeoutMma);
           ok = false;
         }
@@ -427,9 +497,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
                                 pack_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
                                 pack_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
         } else {
-          float4* dst = reinterpret_cast<float4*>(slot + row_in_group * D + col);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<float4*>(slot + tree_acc_at(row_in_group, col + 4 * e, rows_max)) =
+                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
       };
       auto put_ml = [&](float mm, float ll) {
@@ -480,7 +551,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
       tc::fence_before_sync();
       bar();  // both streams have read O and the exchanged statistics
       if (t256 == 0) tree_note_join(a, pc);
-      k += nt, ++pi;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&piece_free[ps]);
+      k += nt;
     }
   }
 

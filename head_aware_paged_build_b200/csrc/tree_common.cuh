@@ -56,24 +56,21 @@ __device__ __forceinline__ int tree_nodes(const TreeLaunch& a, int b, bool* bad 
   return min(max(n, 0), a.T);
 }
 
-// Ancestor masks (each node itself included) of a sequence's n nodes, by one
-// warp: lane x holds nodes x and x + 32.  Pointer doubling: a round joins each
-// node's mask with that of the farthest ancestor reached so far and jumps
-// there, so a chain of 64 takes six rounds and a shallow tree one or two.  An
-// entry outside [-1, own index) is reported and counts as a root.
-__device__ __forceinline__ void tree_ancestors(const TreeLaunch& a, int b, int n, int lane, uint64_t (&anc)[2]) {
-  int up[2];
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int i = lane + 32 * x;
-    up[x] = -1;
-    anc[x] = uint64_t(1) << i;
-    if (i < n) {
-      const int p = a.parents[int64_t(b) * a.T + i];
-      if (p < -1 || p >= i) record_error(a.status, kDevBadTree);
-      else up[x] = p;
-    }
-  }
+// One parent entry, checked: one outside [-1, own index) is reported and counts as a root.
+__device__ __forceinline__ int tree_parent(const TreeLaunch& a, int b, int n, int i) {
+  if (i >= n) return -1;
+  const int p = a.parents[int64_t(b) * a.T + i];
+  if (p >= -1 && p < i) return p;
+  record_error(a.status, kDevBadTree);
+  return -1;
+}
+// Ancestor masks (each node itself included) by one warp: lane x holds nodes x
+// and x + 32, up[] their parents.  Pointer doubling: a round joins each node's
+// mask with that of the farthest ancestor reached so far and jumps there, so a
+// chain of 64 takes six rounds and a shallow tree two or three.
+__device__ __forceinline__ void tree_ancestors(int up0, int up1, int lane, uint64_t (&anc)[2]) {
+  int up[2] = {up0, up1};
+  anc[0] = uint64_t(1) << lane, anc[1] = uint64_t(1) << (lane + 32);
   while (__any_sync(0xffffffffu, up[0] >= 0 || up[1] >= 0)) {
     uint64_t m[2];
     int next[2];
@@ -109,19 +106,17 @@ __device__ __forceinline__ uint64_t tree_visible(uint64_t mask, const HeadDesc& 
   return mask & ~hidden;
 }
 
-// One warp writes the draft's n rows as a page of 64 slots in shared memory:
-// K in blocks of 64 dimensions k_block bytes apart (bf16; E4M3 pages are one
-// block), V transposed, both as an append lays them out; slots behind n hold
-// zeros in V (their weights are zero, and 0 x garbage must stay 0) and are left
-// as they are in K (their scores are masked).  Loads go out in batches: the
-// rows come from global memory, and one row at a time would cost its latency
-// up to 64 times.
+// The draft's n rows as a page of 64 slots in shared memory, as an append lays
+// them out; one warp each for K (in blocks of 64 dimensions k_block bytes apart;
+// E4M3 pages are one block) and V (transposed).  Slots behind n hold zeros in V
+// (their weights are zero, and 0 x garbage must stay 0) and are left as they are
+// in K (their scores are masked).  Loads go out in batches: the rows come from
+// global memory, and one row at a time would cost its latency up to 64 times.
 template <int D, bool FP8>
-__device__ __forceinline__ void tree_draft_page(const TreeLaunch& a, const HeadDesc& hd, int n, uint8_t* kdst,
-                                                int k_block, uint8_t* vdst, int lane) {
-  const int64_t base = int64_t(hd.b) * a.ds_seq + int64_t(hd.kv) * a.ds_head;
-  const __nv_bfloat16* kn = static_cast<const __nv_bfloat16*>(a.k_draft) + base;
-  const __nv_bfloat16* vn = static_cast<const __nv_bfloat16*>(a.v_draft) + base;
+__device__ __forceinline__ void tree_draft_k(const TreeLaunch& a, const HeadDesc& hd, int n, uint8_t* kdst,
+                                             int k_block, int lane) {
+  const __nv_bfloat16* kn =
+      static_cast<const __nv_bfloat16*>(a.k_draft) + int64_t(hd.b) * a.ds_seq + int64_t(hd.kv) * a.ds_head;
   constexpr int CR = D / 8, KB = 8;  // 16-byte chunks of a K row; loads in flight
   for (int u0 = lane; u0 < n * CR; u0 += 32 * KB) {
     uint4 v[KB];
@@ -152,7 +147,12 @@ __device__ __forceinline__ void tree_draft_page(const TreeLaunch& a, const HeadD
       }
     }
   }
-  // V: a lane takes two dimensions of a run of tokens and writes a 16-byte chunk of each
+}
+template <int D, bool FP8>
+__device__ __forceinline__ void tree_draft_v(const TreeLaunch& a, const HeadDesc& hd, int n, uint8_t* vdst, int lane) {
+  const __nv_bfloat16* vn =
+      static_cast<const __nv_bfloat16*>(a.v_draft) + int64_t(hd.b) * a.ds_seq + int64_t(hd.kv) * a.ds_head;
+  // a lane takes two dimensions of a run of tokens and writes a 16-byte chunk of each
   constexpr int DP = D / 2, TG = FP8 ? 16 : 8;
 #pragma unroll 2
   for (int u = lane; u < DP * (64 / TG); u += 32) {
@@ -205,9 +205,10 @@ struct TreeSplit {
     int32_t groups;  // row groups
     int64_t per;     // units of one row group
   };
-  __device__ __forceinline__ static Weight weight(const TreeLaunch& a, int kind, int ctx_len, int n_vpages, int b) {
+  __device__ __forceinline__ static Weight weight(const TreeLaunch& a, int kind, int ctx_len, int n_vpages, int b,
+                                                   bool* bad = nullptr) {
     Weight w;
-    w.n = tree_nodes(a, b);
+    w.n = tree_nodes(a, b, bad);
     w.live = kind == 0 ? min(n_vpages, (ctx_len + a.P - 1) / a.P) : n_vpages;
     w.pages = w.live + (w.n + a.P - 1) / a.P;
     w.groups = (w.n + a.nodes_per_group - 1) / a.nodes_per_group;
@@ -216,12 +217,10 @@ struct TreeSplit {
   }
   __device__ __forceinline__ static int64_t head_units(const TreeLaunch& a, int h) {
     const HeadDesc* d = a.heads + h;
-    if (blockIdx.x == 0 && d->kv == 0) {
-      bool bad = false;
-      tree_nodes(a, d->b, &bad);
-      if (bad) record_error(a.status, kDevBadTree);
-    }
-    const Weight w = weight(a, d->kind, d->ctx_len, d->n_vpages, d->b);
+    const int b = h / a.num_kv_heads;  // heads are in (sequence, kv-head) order
+    bool bad = false;
+    const Weight w = weight(a, d->kind, d->ctx_len, d->n_vpages, b, &bad);
+    if (bad && blockIdx.x == 0) record_error(a.status, kDevBadTree);
     return w.per * w.groups;
   }
   __device__ __forceinline__ int64_t cut(int64_t c) const { return c * units / ctas; }
@@ -335,9 +334,34 @@ struct TreeSplit {
   }
 };
 
-// Floats of a partial slot: acc [rows][D], then (m, l) of each row; 16-byte aligned.
+// A partial slot: the accumulators in chunks of four columns, [D / 4][rows][4],
+// then (m, l) of each row.  (A thread holds a row, or eight lanes hold eight: in
+// row order a warp's store would touch a line a row.)  16-byte aligned.
 __device__ __forceinline__ int64_t tree_slot_floats(const TreeLaunch& a) {
   return partial_slot_floats(a.nodes_per_group * a.group, a.D);
+}
+__device__ __forceinline__ int64_t tree_acc_at(int row, int col, int rows_max) {
+  return (int64_t(col >> 2) * rows_max + row) * 4 + (col & 3);
+}
+
+// A piece as the producer warp hands it to the others, a slot ahead, so that
+// nobody else waits for the table: the table's entries, the sequence's checked
+// parents and the number of ring stages used before it.  head < 0: no more.
+template <typename Piece>
+struct TreePieceInfo {
+  Piece pc;
+  int32_t stage0;
+  int8_t up[kMaxTreeNodes];
+};
+// The producer warp's writing of it (the caller signals it).
+template <typename Piece>
+__device__ __forceinline__ void tree_publish(const TreeLaunch& a, const Piece& pc, int stage0, int lane,
+                                             TreePieceInfo<Piece>& out) {
+#pragma unroll
+  for (int x = 0; x < 2; ++x)
+    out.up[lane + 32 * x] = int8_t(tree_parent(a, pc.hd.b, pc.n, lane + 32 * x));
+  if (lane == 0) out.pc = pc, out.stage0 = stage0;
+  __syncwarp();
 }
 
 // What the joining kernel needs of this CTA: the row group that starts in it
