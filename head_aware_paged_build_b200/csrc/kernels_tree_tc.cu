@@ -3,30 +3,32 @@
 //
 // One persistent CTA an SM walks its pieces of the work line (tree_common.cuh).
 // A query tile is up to 128 rows (nodes x the group's q-heads, TMEM lane = row),
-// a KV tile two pages, 128 tokens.  Two softmax streams share the tensor core:
-//   a piece of one query tile   stream x takes KV tiles x, x + 2, ... with its own
+// a KV tile one page, 64 tokens.  Two softmax streams share the tensor core:
+//   a piece of one query tile   stream x takes pages x, x + 2, ... with its own
 //                               running maximum, sum and O; the streams' results
 //                               join at the end of the piece;
-//   a piece of two query tiles  (kWide) stream x takes query tile x over every
-//                               KV tile, so one staged tile feeds 256 rows.
-// Either way the tensor core works for one stream while the other's softmax runs:
-//   S_x = Q K^T, then  O_x += P_x V, S_x (next), O_1-x += ..., alternating.
-// One query tile reads its K/V once and is bound by HBM (64 KB a tile take
-// 1.5 us of an SM's share, its two products 0.75 us); two tiles a CTA double the
-// products on the same bytes.
+//   a piece of two query tiles  (WIDE) stream x takes query tile x over every
+//                               page, so one staged page feeds 256 rows.
+// A stream has two S buffers of 64 columns: while its softmax works on one page's
+// scores, the tensor core makes the next page's S and the last one's O += P V.
+// (With one buffer of 128 tokens a stream, a softmax waited for its own two
+// products: 251 us where this form takes 222 on 64 nodes of the 32K layer.)
+// One query tile reads its K/V once and is bound by HBM; two tiles a CTA double
+// the products on the same bytes and are bound by the softmax's arithmetic.
 //
-// Warp roles (384 threads; the first warpgroup's spare registers go to the
-// softmax threads):
-//   warp 0     producer: walks the CTA's pieces and hands each to the others a slot
-//              ahead; Q tiles by TMA (128-byte swizzle), K and V pages by bulk copies
-//              into a ring of stages (pool pages are stored as the tensor cores' operands)
-//   warp 1     TMEM owner and MMA issuer (one thread)
-//   warps 2, 3 the draft's K and V rows, written as one more page of a stage
-//   warps 4-7  softmax of stream 0, warps 8-11 of stream 1: a thread a row, the
-//              whole 128-score row in registers; lazy rescale of O (only when the
-//              row's maximum grows by more than 2^8), P written as bf16 over S
-// The commit that signals S_x(j) also covers stream x's earlier O += P V, so a
-// softmax thread that holds S_x(j) may rescale O_x with no further wait.
+// Warp roles (384 threads):
+//   warp 0     walks the CTA's pieces and hands each to the others a slot ahead; Q
+//              tiles by TMA (128-byte swizzle), K pages by bulk copies into a ring
+//              (pool pages are stored as the tensor cores' operands), the draft's K
+//              rows written as one more page
+//   warps 1, 3 MMA issuers of the two streams (one thread each), so that one
+//              stream's waits and commits pass while the other's products run;
+//              warp 1 owns the TMEM
+//   warp 2     V pages, and the draft's V rows, into a ring of their own: a K page is
+//              free after S, a V page only a softmax and O += P V later
+//   warps 4-7  softmax of stream 0, warps 8-11 of stream 1: a thread a row; lazy
+//              rescale of O (only when the row's maximum grows by more than 2^8), P
+//              written as bf16 over the page's own S
 // Sums, maxima and O are fp32; P is rounded to bf16, V's own type.
 // Every wait is bounded; one that runs out records a status code, and the CTA
 // drains its copies and MMAs, frees its TMEM and returns.
@@ -41,73 +43,86 @@ namespace sp {
 namespace {
 
 constexpr int kThreads = 384;
-// Registers a thread: 168 at launch (x 384 threads = 64512); 88 x 128 + 208 x 256 = 64512.
-constexpr int kRegsIssue = 88, kRegsSoftmax = 208;
 constexpr int kSoftmaxThreads = 256;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.f;
 constexpr uint32_t kAll = 0xffffffffu;
-// One exponent pair in every kPolyPeriod is computed on the FMA pipe.
-constexpr int kPolyPeriod = 8;
+// Exponent pairs (of every eight) computed on the FMA pipe, next to the SFU's.
+constexpr uint32_t kPolyMask = 0b10010000;
+// Page descriptions in flight: a K page's place is free once its S is made, so
+// the producer is at most KS pages ahead of S, and S four pages ahead of the
+// softmax that reads the description.
+constexpr int kDescs = 16;
 
 template <int D, bool WIDE>
 struct TreeTc {
   static constexpr int kQ = D / 64 * 16384;  // a query tile: [D/64][128 rows][128 B]
-  static constexpr int kK = D / 64 * 16384;  // [D/64][128 tokens][128 B]
-  static constexpr int kV = 2 * D * 128;     // [2 pages][D rows][64 tokens * 2 B]
-  static constexpr int kStage = kK + kV;
+  static constexpr int kPage = 64 * D * 2;   // a K page [D/64][64 tokens][128 B], a V page [D rows][128 B]
   static constexpr int kQTiles = WIDE ? 2 : 1;
-  static constexpr int NS = (D == 128 ? 3 : 6) - (WIDE ? 1 : 0);
-  static constexpr int kOffStage = kQTiles * kQ;
-  static constexpr int kOffMl = kOffStage + NS * kStage;  // (m, l) of each row and stream
+  // the 224 KB that Q leaves, in pages: K waits for its copy alone, V for a softmax too
+  static constexpr int KS = D == 128 ? (WIDE ? 3 : 4) : 8, VS = D == 128 ? (WIDE ? 5 : 8) : 12;
+  static constexpr int kOffK = kQTiles * kQ;
+  static constexpr int kOffV = kOffK + KS * kPage;
+  static constexpr int kOffMl = kOffV + VS * kPage;  // (m, l) of each row and stream
   static constexpr int kOffDesc = kOffMl + 2 * 128 * 8;
-  static constexpr int kOffInfo = kOffDesc + NS * 2 * 16;
-  using Split = TreeSplit<2, 2, 3>;
+  static constexpr int kOffInfo = kOffDesc + kDescs * 8;
+  using Split = TreeSplit<1, 4, 6>;
   using Info = TreePieceInfo<typename Split::Piece>;
   static constexpr int kOffBar = kOffInfo + (2 * int(sizeof(Info)) + 7) / 8 * 8;
-  static constexpr int kBytes = kOffBar + (14 + 2 * NS) * 8 + 8;
+  static constexpr int kBytes = kOffBar + (20 + 2 * KS + 2 * VS) * 8 + 8;
+  static_assert(KS + 4 <= kDescs, "page descriptions");
   static_assert(kBytes <= 232448, "shared memory of a CTA");
-  static_assert(kOffStage % 1024 == 0 && kStage % 1024 == 0 && kOffMl % 8 == 0 && kOffDesc % 16 == 0 &&
+  static_assert(kOffK % 1024 == 0 && kPage % 1024 == 0 && kOffMl % 8 == 0 && kOffDesc % 8 == 0 &&
                     kOffInfo % alignof(Info) == 0 && kOffBar % 8 == 0,
                 "alignment of the shared-memory parts");
   static_assert((kThreads / 32 + 2) * 8 <= 2 * 128 * 8, "the split's scratch lies in the statistics' place");
 };
+
+// What the softmax needs of a page: its first position and its valid slots
+// (lo | hi << 16); 0: no slot is seen.
+struct PageSlots {
+  int32_t abs_start;
+  int32_t span;
+};
+constexpr int32_t kSlotsAll = -1;    // every row sees every slot
+constexpr int32_t kSlotsDraft = -2;  // the draft's page
 
 template <int D, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, TreeLaunch a) {
   using C = TreeTc<D, WIDE>;
   using Split = typename C::Split;
   using Info = typename C::Info;
-  constexpr int NS = C::NS;
+  constexpr int KS = C::KS, VS = C::VS, kUses = WIDE ? 2 : 1;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* stage_s = smem + C::kOffStage;
+  uint8_t *k_ring = smem + C::kOffK, *v_ring = smem + C::kOffV;
   float2* ml_s = reinterpret_cast<float2*>(smem + C::kOffMl);
-  PageDesc* sdesc = reinterpret_cast<PageDesc*>(smem + C::kOffDesc);
+  PageSlots* slots_s = reinterpret_cast<PageSlots*>(smem + C::kOffDesc);
   Info* info = reinterpret_cast<Info*>(smem + C::kOffInfo);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  uint64_t *q_full = bars, *q_free = bars + 1, *o_done = bars + 2, *done = bars + 3;
-  uint64_t *s_full = bars + 4, *p_full = bars + 6, *piece_full = bars + 8, *piece_free = bars + 10;
-  uint64_t *draft_go = bars + 12, *kv_full = bars + 14, *kv_free = kv_full + NS;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(kv_free + NS);
+  uint64_t *q_full = bars, *q_free = bars + 1, *done = bars + 2, *piece_full = bars + 4, *piece_free = bars + 6;
+  // [stream][buffer]: a softmax warp without rows may be a buffer ahead of the others, not two
+  uint64_t *s_full = bars + 8, *p_full = bars + 12;
+  uint64_t *pv_done = bars + 16, *o_done = bars + 18;  // a piece's last but one O += P V of a stream, and its last
+  uint64_t *k_full = bars + 20, *k_free = k_full + KS, *v_full = k_free + KS, *v_free = v_full + VS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_free + VS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
-    mbar_init(q_free, 1);
-    mbar_init(o_done, 1);
-    mbar_init(done, 1);
+    mbar_init(q_free, 2);
     for (int x = 0; x < 2; ++x) {
-      mbar_init(&s_full[x], 1);
-      mbar_init(&p_full[x], 128);
+      mbar_init(&done[x], 1);
+      mbar_init(&s_full[2 * x], 1), mbar_init(&s_full[2 * x + 1], 1);
+      mbar_init(&p_full[2 * x], 4), mbar_init(&p_full[2 * x + 1], 4);
+      mbar_init(&pv_done[x], 1);
+      mbar_init(&o_done[x], 1);
       mbar_init(&piece_full[x], 1);
-      mbar_init(&draft_go[x], 1);
-      mbar_init(&piece_free[x], 8 + 1 + 2);  // softmax warps, MMA issuer, draft warps
+      mbar_init(&piece_free[x], 8 + 3);  // softmax warps; MMA issuers, V producer
     }
-    for (int s = 0; s < NS; ++s) {
-      mbar_init(&kv_full[s], 3);  // the producer and the draft's two writers (without a draft it arrives for them)
-      mbar_init(&kv_free[s], 1);
-    }
+    // a page of two query tiles is free when both issuers' products have read it (of one: its stream's, kUses times)
+    for (int s = 0; s < KS; ++s) mbar_init(&k_full[s], 1), mbar_init(&k_free[s], kUses);
+    for (int s = 0; s < VS; ++s) mbar_init(&v_full[s], 1), mbar_init(&v_free[s], kUses);
     *abort_flag = 0;
     fence_barrier_init();
     tc::prefetch_tensormap(&qmap);
@@ -122,244 +137,229 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  // TMEM columns: S / P of stream x at [128 x, 128 x + 128); O at 256 + x D
-  auto t_s = [&](int x) { return tmem + uint32_t(128 * x); };
+  // TMEM columns: S / P buffer b of stream x at 128 x + 64 b; O at 256 + x D
+  auto t_s = [&](int x, int b) { return tmem + uint32_t(128 * x + 64 * b); };
   auto t_o = [&](int x) { return tmem + uint32_t(256 + x * D); };
   auto fail = [&](int32_t code) {
     record_error(a.status, code);
     *abort_flag = 1;
   };
   const int G = a.group, npt = a.nodes_per_tile;
-  int k = 0;   // KV tiles of the earlier pieces
+  int k = 0;   // pages of the earlier pieces
   int pi = 0;  // pieces so far
   bool ok = true;
 
-  if (warp < 4) {
-    tc::reg_dealloc<kRegsIssue>();
+  if (warp == 0 || warp == 2) {
+    // A producer's pages: records fetched 32 at a time, a lane each; kDraftPage for the draft's, kNoPage for an
+    // empty record or a page id outside the pool.
+    int4 mine = make_int4(0, 0, 0, 0);
+    auto fetch = [&](const typename Split::Piece& pc, int p) {
+      if (p + lane < min(pc.live, pc.p1))
+        mine = *reinterpret_cast<const int4*>(a.pages + pc.hd.vpage_begin + p + lane);
+    };
+    auto page = [&](const typename Split::Piece& pc, int p) {
+      const int i = (p - pc.p0) & 31;
+      if (i == 0 && p > pc.p0) fetch(pc, p);
+      const PageDesc rec{__shfl_sync(kAll, mine.x, i), __shfl_sync(kAll, mine.y, i), __shfl_sync(kAll, mine.z, i), 0};
+      if (p >= pc.live) return PageDesc{kDraftPage, 0, 0, 0};
+      if (slot_hi(rec) <= slot_lo(rec)) return PageDesc{kNoPage, 0, 0, 0};
+      if (rec.phys >= 0 && rec.phys < a.pool_pages) return rec;
+      if (lane == 0) record_error(a.status, kDevBadPage);  // corrupted table: report, read nothing there
+      return PageDesc{kNoPage, 0, 0, 0};
+    };
+    // a wait by lane 0, its outcome for the warp
+    auto wait0 = [&](uint64_t* bar, int parity, int32_t code) {
+      ok = __shfl_sync(kAll, int(lane == 0 && mbar_wait(bar, parity)), 0);
+      if (!ok && lane == 0) fail(code);
+      return ok;
+    };
     if (warp == 0) {
-      // ------------------------------ producer ------------------------------
+      // ------------------------------ pieces, Q and K ------------------------------
       const uint8_t* kpool = static_cast<const uint8_t*>(a.kpool);
-      const uint8_t* vpool = static_cast<const uint8_t*>(a.vpool);
       typename Split::Walk walk = split.walk();
       typename Split::Piece pc;
-      auto piece_slot = [&] {  // the next piece's slot, once it is free
-        const int ps = pi & 1;
-        ok = pi < 2 || __shfl_sync(kAll, int(lane == 0 && mbar_wait(&piece_free[ps], ((pi >> 1) - 1) & 1)), 0);
-        if (!ok && lane == 0) fail(kDevTimeoutEmpty);
-        return ps;
-      };
+      auto slot_free = [&] { return pi < 2 || wait0(&piece_free[pi & 1], ((pi >> 1) - 1) & 1, kDevTimeoutEmpty); };
       while (ok && split.next(a, walk, pc)) {
         const bool two = WIDE && pc.nodes > npt;
-        const PageDesc* rec = a.pages + pc.hd.vpage_begin;
-        int4 mine = make_int4(0, 0, 0, 0);
-        if (pc.p0 + lane < pc.live) mine = *reinterpret_cast<const int4*>(rec + pc.p0 + lane);
-        const int ps = piece_slot();
-        if (!ok) break;
-        tree_publish(a, pc, k, lane, info[ps]);
-        if (lane == 0) {
-          mbar_arrive(&piece_full[ps]);
-          if (pc.p1 <= pc.live) mbar_arrive(&draft_go[ps]);  // no draft page in this piece
-        }
-        auto load_q = [&] {  // behind the first KV tiles: its place is free only after the previous piece's last S
+        fetch(pc, pc.p0);
+        if (!slot_free()) break;
+        tree_publish(a, pc, k, lane, info[pi & 1]);
+        if (lane == 0) mbar_arrive(&piece_full[pi & 1]);
+        const int p_last = pc.hd.ctx_len + pc.n - 1;
+        for (int p = pc.p0; p < pc.p1; ++p, ++k) {
+          const int st = k % KS;
+          uint8_t* k_s = k_ring + st * C::kPage;
+          const PageDesc pg = page(pc, p);
+          if (k >= KS && !wait0(&k_free[st], ((k / KS) - 1) & 1, kDevTimeoutEmpty)) break;
+          if (pg.phys == kDraftPage) {
+            tree_draft_k<D, false>(a, pc.hd, pc.n, k_s, 8192, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
           if (lane == 0) {
-            ok = pi == 0 || mbar_wait(q_free, (pi - 1) & 1);
-            if (ok) {
+            slots_s[k % kDescs] =
+                PageSlots{pg.abs_start, pg.phys == kDraftPage                                      ? kSlotsDraft
+                                        : pg.phys >= 0 && tree_page_full(pg, pc.hd, p_last) ? kSlotsAll
+                                                                                            : pg.span};
+            if (pg.phys >= 0) {
+              mbar_arrive_expect_tx(&k_full[st], C::kPage);
+              bulk_g2s(k_s, kpool + int64_t(pg.phys) * a.page_bytes, C::kPage, &k_full[st]);
+            } else {
+              mbar_arrive(&k_full[st]);
+            }
+          }
+          __syncwarp();
+          if (p == pc.p0) {  // behind the first K page: Q's place is free only after the previous piece's last S
+            if (pi > 0 && !wait0(q_free, (pi - 1) & 1, kDevTimeoutMma)) break;
+            if (lane == 0) {
               mbar_arrive_expect_tx(q_full, (two ? 2 : 1) * (D / 64) * npt * G * 128);
               for (int x = 0; x < (two ? 2 : 1); ++x)
 #pragma unroll
                 for (int h = 0; h < D / 64; ++h)
                   tc::tma_load_3d(smem + x * C::kQ + h * 16384, &qmap, h * 64, pc.hd.kv * G,
                                   pc.hd.b * a.T + pc.node0 + x * npt, q_full);
-            } else {
-              fail(kDevTimeoutMma);
             }
-          }
-          ok = __shfl_sync(kAll, int(ok), 0);
-        };
-        const int nt = (pc.p1 - pc.p0 + 1) / 2;
-        for (int j = 0; ok && j < nt; ++j, ++k) {
-          const int st = k % NS;
-          uint8_t* k_s = stage_s + st * C::kStage;
-          uint8_t* v_s = k_s + C::kK;
-          PageDesc pg[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int p = pc.p0 + 2 * j + h, i = (2 * j + h) & 31;
-            if (i == 0 && p > pc.p0 && p + lane < pc.live) mine = *reinterpret_cast<const int4*>(rec + p + lane);
-            pg[h] = PageDesc{__shfl_sync(kAll, mine.x, i), __shfl_sync(kAll, mine.y, i), __shfl_sync(kAll, mine.z, i),
-                             0};
-            if (p >= pc.live) pg[h] = PageDesc{p == pc.live && p < pc.p1 ? kDraftPage : kNoPage, 0, 0, 0};
-            else if (p >= pc.p1 || slot_hi(pg[h]) <= slot_lo(pg[h])) pg[h] = PageDesc{kNoPage, 0, 0, 0};
-            else if (pg[h].phys < 0 || pg[h].phys >= a.pool_pages) {
-              if (lane == 0) record_error(a.status, kDevBadPage);  // corrupted table: read nothing there
-              pg[h] = PageDesc{kNoPage, 0, 0, 0};
-            }
-          }
-          if (k >= NS) ok = __shfl_sync(kAll, int(lane == 0 && mbar_wait(&kv_free[st], ((k / NS) - 1) & 1)), 0);
-          if (!ok) {
-            if (lane == 0) fail(kDevTimeoutEmpty);
-            break;
-          }
-          int bytes = 0;
-          bool draft = false;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (pg[h].phys >= 0) bytes += (C::kK + C::kV) / 2;
-            else if (pg[h].phys == kDraftPage) draft = true;
-            else {  // no page: weights of zero meet values of zero
-              for (int e = lane; e < D * 8; e += 32)
-                reinterpret_cast<uint4*>(v_s + h * (D * 128))[e] = make_uint4(0, 0, 0, 0);
-              fence_proxy_async_smem();
-            }
-          }
-          __syncwarp();
-          if (lane == 0) {
-            sdesc[2 * st] = pg[0], sdesc[2 * st + 1] = pg[1];
-            mbar_arrive_expect_tx(&kv_full[st], bytes);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (pg[h].phys < 0) continue;
-              const int64_t off = int64_t(pg[h].phys) * a.page_bytes;
-#pragma unroll
-              for (int c = 0; c < D / 64; ++c)
-                bulk_g2s(k_s + c * 16384 + h * 8192, kpool + off + c * 8192, 8192, &kv_full[st]);
-              bulk_g2s(v_s + h * (D * 128), vpool + off, D * 128, &kv_full[st]);
-            }
-            if (draft) mbar_arrive(&draft_go[ps]);  // the stage is free
-            else mbar_arrive(&kv_full[st]), mbar_arrive(&kv_full[st]);
-          }
-          __syncwarp();
-          if (j == min(1, nt - 1)) {
-            load_q();
-            if (ok) ++pi;
+            __syncwarp();
+            ++pi;
           }
         }
       }
-      if (ok) {
-        const int ps = piece_slot();
-        if (ok && lane == 0) {
-          info[ps].pc.head = -1;
-          mbar_arrive(&piece_full[ps]);
-        }
+      if (ok && slot_free() && lane == 0) {
+        info[pi & 1].pc.head = -1;
+        mbar_arrive(&piece_full[pi & 1]);
       }
       // drain: never leave with copies still writing this CTA's shared memory
       if (lane == 0) {
         if (pi > 0) mbar_wait(q_full, (pi - 1) & 1);
-        for (int j = (k > NS ? k - NS : 0); j < k; ++j)
-          if (!mbar_wait(&kv_full[j % NS], (j / NS) & 1)) break;
+        for (int j = (k > KS ? k - KS : 0); j < k; ++j)
+          if (!mbar_wait(&k_full[j % KS], (j / KS) & 1)) break;
       }
-    } else if (warp == 1) {
-      // ------------------------------ MMA issuer ------------------------------
-      if (lane == 0) {
-        constexpr uint32_t idesc_s = tc::idesc_bf16_f32(128, 128);
-        constexpr uint32_t idesc_o = tc::idesc_bf16_f32(128, D);
-        const uint32_t q_addr = smem_u32(smem), st_addr = smem_u32(stage_s);
-        uint32_t turn[2] = {0, 0};  // P tiles taken of each stream
-        auto wait_kv = [&](int tile) {
-          if (mbar_wait(&kv_full[tile % NS], (tile / NS) & 1)) return true;
-          fail(kDevTimeoutFull);
-          return false;
-        };
-        auto issue_s = [&](int x, int q, int tile) {
-          const uint64_t qd = tc::smem_desc_sw128(q_addr + q * C::kQ);
-          const uint64_t kd = tc::smem_desc_sw128(st_addr + (tile % NS) * C::kStage);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-            tc::mma_bf16_ss(t_s(x), qd + off, kd + off, idesc_s, kk > 0);
-          }
-          tc::commit(&s_full[x]);
-        };
-        auto issue_pv = [&](int x, int tile, bool acc) {
-          const uint64_t vd = tc::smem_desc_sw128(st_addr + (tile % NS) * C::kStage + C::kK);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            tc::mma_bf16_ts(t_o(x), t_s(x) + kk * 8, vd + (((kk >> 2) * (D * 128) + (kk & 3) * 32) >> 4), idesc_o,
-                            (acc || kk > 0) ? 1u : 0u);
-        };
-        while (ok) {
-          const int ps = pi & 1;
-          if (!mbar_wait(&piece_full[ps], (pi >> 1) & 1)) {
-            fail(kDevTimeoutFull);
-            break;
-          }
-          if (info[ps].pc.head < 0) break;
-          const bool two = WIDE && info[ps].pc.nodes > npt;
-          const int nt = (info[ps].pc.p1 - info[ps].pc.p0 + 1) / 2, U = two ? 2 * nt : nt;
-          mbar_arrive(&piece_free[ps]);
-          auto tile_of = [&](int u) { return k + (two ? u >> 1 : u); };
-          if (!mbar_wait(q_full, pi & 1)) {
-            fail(kDevTimeoutFull);
-            break;
-          }
-          for (int u = 0; ok && u < min(2, U); ++u) {
-            ok = wait_kv(tile_of(u));
-            if (!ok) break;
-            tc::fence_after_sync();
-            issue_s(u, two ? u : 0, tile_of(u));
-          }
-          if (ok && U <= 2) tc::commit(q_free);
-          for (int u = 0; ok && u < U; ++u) {
-            const int x = u & 1;
-            if (*abort_flag || !mbar_wait(&p_full[x], turn[x] & 1)) {
-              fail(kDevTimeoutSoftmax);
-              ok = false;
-              break;
-            }
-            ++turn[x];
-            tc::fence_after_sync();
-            issue_pv(x, tile_of(u), u >= 2);
-            if (!two || x == 1) tc::commit(&kv_free[tile_of(u) % NS]);
-            if (u + 2 < U) {
-              ok = wait_kv(tile_of(u + 2));
-              if (!ok) break;
-              tc::fence_after_sync();
-              issue_s(x, two ? x : 0, tile_of(u + 2));
-              if (u + 3 == U) tc::commit(q_free);
-            }
-          }
-          if (!ok) break;
-          tc::commit(o_done);
-          k += nt, ++pi;
-        }
-        // all MMAs issued by this thread complete before TMEM is released
-        tc::commit(done);
-        mbar_wait(done, 0);
-      }
-      __syncwarp();
     } else {
-      // ------------------------------ draft page ------------------------------
-      for (;; ++pi) {
+      // ------------------------------ V ------------------------------
+      const uint8_t* vpool = static_cast<const uint8_t*>(a.vpool);
+      for (; ok; ++pi) {
         const int ps = pi & 1;
-        if (!__all_sync(kAll, mbar_wait(&piece_full[ps], (pi >> 1) & 1))) break;
-        const Info& in = info[ps];
-        if (in.pc.head < 0) break;
-        if (in.pc.p1 > in.pc.live) {
-          const int at = in.pc.p1 - 1 - in.pc.p0, tile = in.stage0 + at / 2, h = at & 1, st = tile % NS;
-          // the producer has seen the stage free (a wait on the stage's own barrier could be phases ahead of it)
-          if (!__all_sync(kAll, mbar_wait(&draft_go[ps], (pi >> 1) & 1))) break;
-          uint8_t* k_s = stage_s + st * C::kStage;
-          if (warp == 2) tree_draft_k<D, false>(a, in.pc.hd, in.pc.n, k_s + h * 8192, 16384, lane);
-          else tree_draft_v<D, false>(a, in.pc.hd, in.pc.n, k_s + C::kK + h * (D * 128), lane);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&kv_full[st]);
-        }
+        if (!wait0(&piece_full[ps], (pi >> 1) & 1, kDevTimeoutFull) || info[ps].pc.head < 0) break;
+        const typename Split::Piece pc = info[ps].pc;
         __syncwarp();
         if (lane == 0) mbar_arrive(&piece_free[ps]);
+        fetch(pc, pc.p0);
+        for (int p = pc.p0; p < pc.p1; ++p, ++k) {
+          const int st = k % VS;
+          uint8_t* v_s = v_ring + st * C::kPage;
+          const PageDesc pg = page(pc, p);
+          if (k >= VS && !wait0(&v_free[st], ((k / VS) - 1) & 1, kDevTimeoutEmpty)) break;
+          if (pg.phys < 0) {
+            if (pg.phys == kDraftPage) {
+              tree_draft_v<D, false>(a, pc.hd, pc.n, v_s, lane);
+            } else {  // no page: weights of zero meet values of zero
+              for (int e = lane; e < C::kPage / 16; e += 32)
+                reinterpret_cast<uint4*>(v_s)[e] = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (lane == 0) {
+            if (pg.phys >= 0) {
+              mbar_arrive_expect_tx(&v_full[st], C::kPage);
+              bulk_g2s(v_s, vpool + int64_t(pg.phys) * a.page_bytes, C::kPage, &v_full[st]);
+            } else {
+              mbar_arrive(&v_full[st]);
+            }
+          }
+          __syncwarp();
+        }
       }
+      if (lane == 0)
+        for (int j = (k > VS ? k - VS : 0); j < k; ++j)
+          if (!mbar_wait(&v_full[j % VS], (j / VS) & 1)) break;
+    }
+  } else if (warp < 4) {
+    if (lane == 0) {
+      // ------------------------------ MMA issuers ------------------------------
+      const int x = warp >> 1;  // stream
+      constexpr uint32_t idesc_s = tc::idesc_bf16_f32(128, 64);
+      constexpr uint32_t idesc_o = tc::idesc_bf16_f32(128, D);
+      const uint32_t q_addr = smem_u32(smem), k_addr = smem_u32(k_ring), v_addr = smem_u32(v_ring);
+      uint32_t phase = 0;  // bit b: parity of the phase of the stream's P buffer b
+      auto wait = [&](uint64_t* bar, int parity, int32_t code) {
+        ok = mbar_wait(bar, parity);
+        if (!ok) fail(code);
+        return ok;
+      };
+      // the stream's last product of a page is issued: its place is free when that has run
+      auto free_page = [&](uint64_t* bar, bool two) {
+        tc::commit(bar);
+        if (WIDE && !two) tc::commit(bar);
+      };
+      while (ok) {
+        const int ps = pi & 1;
+        if (!wait(&piece_full[ps], (pi >> 1) & 1, kDevTimeoutFull) || info[ps].pc.head < 0) break;
+        const bool two = WIDE && info[ps].pc.nodes > npt;
+        const int np = info[ps].pc.p1 - info[ps].pc.p0, U = two ? np : (np + 1 - x) / 2;
+        mbar_arrive(&piece_free[ps]);
+        auto page_of = [&](int u) { return k + (two ? u : 2 * u + x); };
+        const uint64_t qd = tc::smem_desc_sw128(q_addr + (two ? x : 0) * C::kQ);
+        auto issue_s = [&](int u) {
+          const int pg = page_of(u);
+          if (!wait(&k_full[pg % KS], (pg / KS) & 1, kDevTimeoutFull)) return;
+          tc::fence_after_sync();
+          const uint64_t kd = tc::smem_desc_sw128(k_addr + (pg % KS) * C::kPage);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc::mma_bf16_ss(t_s(x, u & 1), qd + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                            kd + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
+          tc::commit(&s_full[2 * x + (u & 1)]);
+          free_page(&k_free[pg % KS], two);
+          if (u == U - 1) tc::commit(q_free);
+        };
+        if (U == 0) {  // a piece of one page
+          mbar_arrive(q_free);
+        } else if (wait(q_full, pi & 1, kDevTimeoutFull)) {
+          issue_s(0);
+          if (ok && U > 1) issue_s(1);
+          for (int u = 0; ok && u < U; ++u) {
+            const int pg = page_of(u);
+            if (!wait(&v_full[pg % VS], (pg / VS) & 1, kDevTimeoutFull)) break;
+            if (!wait(&p_full[2 * x + (u & 1)], phase >> (u & 1) & 1, kDevTimeoutSoftmax)) break;
+            phase ^= 1u << (u & 1);
+            tc::fence_after_sync();
+            const uint64_t vd = tc::smem_desc_sw128(v_addr + (pg % VS) * C::kPage);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc::mma_bf16_ts(t_o(x), t_s(x, u & 1) + kk * 8, vd + ((kk * 32) >> 4), idesc_o,
+                              (u > 0 || kk > 0) ? 1u : 0u);
+            free_page(&v_free[pg % VS], two);
+            // the next S also says that this product is done; the last two have no next S
+            if (u + 2 < U) issue_s(u + 2);
+            else tc::commit(u + 1 < U ? &pv_done[x] : &o_done[x]);
+          }
+        }
+        if (*abort_flag) break;
+        k += np, ++pi;
+      }
+      // all MMAs issued by this thread complete before TMEM is released
+      tc::commit(&done[x]);
+      mbar_wait(&done[x], 0);
     }
   } else {
-    tc::reg_alloc<kRegsSoftmax>();
     // ------------------------------ softmax ------------------------------
     const int x = (warp - 4) >> 2;
     const int quarter = warp & 3;  // TMEM lane quarter this warp may access
     const int r = quarter * 32 + lane;
     const uint32_t lane_off = uint32_t(quarter * 32) << 16;
+    const uint32_t to = t_o(x) + lane_off;
     const int t256 = threadIdx.x - 128;
     const float sl2 = a.scale_log2;
-    uint32_t turn = 0;  // tiles of this stream so far
+    uint32_t phase = 0;  // parities: bits 0, 1 of the stream's S buffers, 2 of pv_done, 3 of o_done
     auto bar = [] { asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory"); };
+    // waits are voted: tcgen05.ld / st need the whole warp
+    auto wait = [&](uint64_t* bar, int bit) {
+      if (ok && !__all_sync(kAll, mbar_wait(bar, phase >> bit & 1))) {
+        fail(kDevTimeoutMma);
+        ok = false;
+      }
+    };
     for (;; ++pi) {
       const int ps = pi & 1;
       // all softmax warps go on, or none: the barriers wait for every one of them
@@ -367,115 +367,106 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
       if (ok && !got) fail(kDevTimeoutFull);
       if (!bar_red_and(1, kSoftmaxThreads, got)) break;
       if (info[ps].pc.head < 0) break;
-      const typename Split::Piece pc = info[ps].pc;
+      const typename Split::Piece& pc = info[ps].pc;
+      const HeadDesc hd = pc.hd;
       const bool two = WIDE && pc.nodes > npt;
-      const int nt = (pc.p1 - pc.p0 + 1) / 2, U = two ? 2 * nt : nt;
+      const int np = pc.p1 - pc.p0, U = two ? np : (np + 1 - x) / 2;
       const int first_node = pc.node0 + (two ? x * npt : 0);
       const int rows = min(npt, pc.node0 + pc.nodes - first_node) * G;
       const bool busy = quarter * 32 < rows;  // any row in this warp
       uint64_t nodes[2];
       tree_ancestors(info[ps].up[lane], info[ps].up[lane + 32], lane, nodes);
       const uint64_t mask = tree_mask_of(nodes, min(first_node + r / G, kMaxTreeNodes - 1));
-      const uint64_t anc = tree_visible(mask, pc.hd);
-      const int pos = pc.hd.ctx_len + __popcll(mask) - 1;
-      const int p_last = pc.hd.ctx_len + pc.n - 1;
+      const uint64_t anc = tree_visible(mask, hd);
+      const int pos = hd.ctx_len + __popcll(mask) - 1;
       float m = -INFINITY, l = 0.f;
-      for (int u = x; u < U; u += 2, ++turn) {
-        const int tile = k + (two ? u >> 1 : u), st = tile % NS;
-        // waits are voted: tcgen05.ld / st need the whole warp
-        // (S_x first: then the stage's phase is this tile's, and its descriptors are read behind that barrier too)
-        if (ok && !__all_sync(kAll, mbar_wait(&s_full[x], turn & 1) && mbar_wait(&kv_full[st], (tile / NS) & 1))) {
-          fail(kDevTimeoutMma);
-          ok = false;
+      auto page_scores = [&](int u, int b) {
+        const PageSlots sl = slots_s[(k + (two ? u : 2 * u + x)) % kDescs];
+        const uint32_t ts = t_s(x, b) + lane_off;
+        tc::fence_after_sync();
+        float w[64];
+        tc::tmem_ld32(ts, *reinterpret_cast<float(*)[32]>(w));
+        tc::tmem_ld32(ts + 32, *reinterpret_cast<float(*)[32]>(w + 32));
+        tc::tmem_wait_ld();
+        if (sl.span != kSlotsAll) {
+          const uint64_t vis = sl.span == kSlotsDraft ? anc : tree_page_mask({0, sl.abs_start, sl.span, 0}, hd, pos);
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (!((vis >> e) & 1)) w[e] = -INFINITY;
         }
-        if (ok && busy) {
-          uint64_t vis[2];
-          bool all = true;
+        float m8[8];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const PageDesc pg = sdesc[2 * st + h];
-            if (pg.phys >= 0 && tree_page_full(pg, pc.hd, p_last)) {
-              vis[h] = ~uint64_t(0);
-            } else {
-              vis[h] = pg.phys == kDraftPage ? anc : pg.phys < 0 ? 0 : tree_page_mask(pg, pc.hd, pos);
-              all = false;
-            }
-          }
-          tc::fence_after_sync();
-          float w[128];
-          auto chunk = [&](int c) -> float(&)[32] { return *reinterpret_cast<float(*)[32]>(w + 32 * c); };
+        for (int i = 0; i < 8; ++i) m8[i] = fmaxf(w[i], w[i + 8]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tc::tmem_ld32(t_s(x) + lane_off + 32 * c, chunk(c));
-          tc::tmem_wait_ld();
-          if (!all) {
+        for (int e = 16; e < 64; e += 16)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const uint32_t bits = uint32_t(vis[c >> 1] >> (32 * (c & 1)));
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!((bits >> e) & 1)) w[32 * c + e] = -INFINITY;
-            }
-          }
-          float m4[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) m4[i] = fmaxf(w[i], w[i + 4]);
-#pragma unroll
-          for (int e = 8; e < 128; e += 8)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) m4[i] = fmax3(m4[i], w[e + i], w[e + 4 + i]);
-          const float mts = fmax3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * sl2;
-          float alpha = 1.f;
-          bool need = false;
+          for (int i = 0; i < 8; ++i) m8[i] = fmax3(m8[i], w[e + i], w[e + 8 + i]);
+        const float mts = fmaxf(fmax3(fmax3(m8[0], m8[1], m8[2]), m8[3], m8[4]), fmax3(m8[5], m8[6], m8[7])) * sl2;
+        // the running reference nearly always holds; where a row of the warp has outgrown it, it moves, and O
+        // follows once the previous product is done (the next page's S says so)
+        float alpha = 1.f;
+        if (__any_sync(kAll, mts > m + kRescaleLog2)) {
           if (mts > m + kRescaleLog2) {
             alpha = fast_exp2(m - mts);
-            need = m != -INFINITY;
             m = mts;
           }
-          if (__any_sync(kAll, need)) {
+          if (u > 0) {
+            if (u + 1 < U) wait(&s_full[2 * x + (b ^ 1)], b ^ 1);
+            else wait(&pv_done[x], 2);
+            if (!ok) return;
+            tc::fence_after_sync();
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
               uint32_t o[16];
-              tc::tmem_ld16(t_o(x) + lane_off + c * 16, o);
+              tc::tmem_ld16(to + c * 16, o);
               tc::tmem_wait_ld();
 #pragma unroll
               for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tc::tmem_st16(t_o(x) + lane_off + c * 16, o);
+              tc::tmem_st16(to + c * 16, o);
             }
           }
-          const float base = m == -INFINITY ? 0.f : m;
-          const uint64_t nbase2 = f2_pack(-base, -base), scale2 = f2_pack(sl2, sl2);
-          uint64_t s2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const uint64_t x2 = f2_fma(f2_pack(w[32 * c + 2 * e], w[32 * c + 2 * e + 1]), scale2, nbase2);
-              float e0, e1;
-              if (e % kPolyPeriod == kPolyPeriod - 1) {
-                exp2_poly_pair(x2, e0, e1);
-              } else {
-                float x0, x1;
-                f2_unpack(x2, x0, x1);
-                e0 = fast_exp2(x0), e1 = fast_exp2(x1);
-              }
-              s2[e & 1] = f2_add(s2[e & 1], f2_pack(e0, e1));
-              pk[e] = pack_bf16x2(e0, e1);
-            }
-            tc::tmem_st16(t_s(x) + lane_off + 16 * c, pk);
-          }
-          float a0, a1;
-          f2_unpack(f2_add(s2[0], s2[1]), a0, a1);
-          l = l * alpha + (a0 + a1);
-          tc::tmem_wait_st();
         }
+        const float base = m == -INFINITY ? 0.f : m;
+        const uint64_t nbase2 = f2_pack(-base, -base), scale2 = f2_pack(sl2, sl2);
+        uint64_t s2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const uint64_t x2 = f2_fma(f2_pack(w[32 * c + 2 * e], w[32 * c + 2 * e + 1]), scale2, nbase2);
+            float e0, e1;
+            if (kPolyMask >> (e % 8) & 1) {
+              exp2_poly_pair(x2, e0, e1);
+            } else {
+              float x0, x1;
+              f2_unpack(x2, x0, x1);
+              e0 = fast_exp2(x0), e1 = fast_exp2(x1);
+            }
+            s2[e & 1] = f2_add(s2[e & 1], f2_pack(e0, e1));
+            pk[e] = pack_bf16x2(e0, e1);
+          }
+          tc::tmem_st16(ts + 16 * c, pk);
+        }
+        float a0, a1;
+        f2_unpack(f2_add(s2[0], s2[1]), a0, a1);
+        l = l * alpha + (a0 + a1);
+        tc::tmem_wait_st();
+      };
+      for (int u = 0; u < U; ++u) {
+        const int b = u & 1;
+        wait(&s_full[2 * x + b], b);
+        phase ^= 1u << b;
+        if (ok && busy) page_scores(u, b);
         tc::fence_before_sync();
-        mbar_arrive(&p_full[x]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[2 * x + b]);
       }
       // ------------------------------ end of the piece ------------------------------
-      if (ok && !__all_sync(kAll, mbar_wait(o_done, pi & 1))) {
-        fail(kDevTimeoutMma);
-        ok = false;
+      if (U > 1) phase ^= 1u << 2;
+      if (U > 0) {
+        wait(&o_done[x], 3);
+        phase ^= 1u << 3;
       }
       tc::fence_after_sync();
       const int row_in_group = two ? x * npt * G + r : r;
@@ -483,8 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
       const bool whole = pc.n_pieces == 1;
       float* slot = a.partial + int64_t(pc.slot) * tree_slot_floats(a);
       const int rows_max = a.nodes_per_group * G;
-      const int64_t at =
-          (int64_t(pc.hd.b) * a.T + first_node + r / G) * a.num_q_heads + pc.hd.kv * G + r % G;
+      const int64_t at = (int64_t(hd.b) * a.T + first_node + r / G) * a.num_q_heads + hd.kv * G + r % G;
       // 32 columns of the row's accumulator, scaled, to the output or the partial slot
       auto put = [&](const float (&o)[32], int col, float inv) {
         if (!valid) return;
@@ -513,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             float o[32];
-            tc::tmem_ld32(t_o(x) + lane_off + 32 * c, o);
+            tc::tmem_ld32(to + 32 * c, o);
             tc::tmem_wait_ld();
             put(o, 32 * c, a.v_scale / l);
           }
@@ -521,7 +511,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         }
       } else {  // join the two streams: each thread takes half of the row's columns
         ml_s[x * 128 + r] = make_float2(m, l);
+        tc::fence_before_sync();
         bar();
+        tc::fence_after_sync();
         if (ok && busy) {
           const float2 o_ml = ml_s[(1 - x) * 128 + r];
           const float M = fmaxf(m, o_ml.x), base = M == -INFINITY ? 0.f : M;
@@ -536,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
             tc::tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] *= f0;
-            if (nt > 1) {  // stream 1 had a tile
+            if (np > 1) {  // stream 1 had a page
               float o1[32];
               tc::tmem_ld32(t_o(1) + lane_off + col, o1);
               tc::tmem_wait_ld();
@@ -549,11 +541,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         }
       }
       tc::fence_before_sync();
-      bar();  // both streams have read O and the exchanged statistics
       if (t256 == 0) tree_note_join(a, pc);
-      __syncwarp();
+      k += np;
+      bar();  // both streams have read O, the exchanged statistics and the piece
       if (lane == 0) mbar_arrive(&piece_free[ps]);
-      k += nt;
     }
   }
 
