@@ -48,7 +48,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.f;
 constexpr uint32_t kAll = 0xffffffffu;
 // Exponent pairs (of every eight) computed on the FMA pipe, next to the SFU's.
-constexpr uint32_t kPolyMask = 0b10010000;
+constexpr uint32_t kPolyMask = 0b10000000;
 // Page descriptions in flight: a K page's place is free once its S is made, so
 // the producer is at most KS pages ahead of S, and S four pages ahead of the
 // softmax that reads the description.
@@ -300,10 +300,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         mbar_arrive(&piece_free[ps]);
         auto page_of = [&](int u) { return k + (two ? u : 2 * u + x); };
         const uint64_t qd = tc::smem_desc_sw128(q_addr + (two ? x : 0) * C::kQ);
+        auto wait_k = [&](int u) {
+          const int pg = page_of(u);
+          return wait(&k_full[pg % KS], (pg / KS) & 1, kDevTimeoutFull);
+        };
         auto issue_s = [&](int u) {
           const int pg = page_of(u);
-          if (!wait(&k_full[pg % KS], (pg / KS) & 1, kDevTimeoutFull)) return;
-          tc::fence_after_sync();
           const uint64_t kd = tc::smem_desc_sw128(k_addr + (pg % KS) * C::kPage);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
@@ -316,11 +318,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         if (U == 0) {  // a piece of one page
           mbar_arrive(q_free);
         } else if (wait(q_full, pi & 1, kDevTimeoutFull)) {
-          issue_s(0);
-          if (ok && U > 1) issue_s(1);
+          for (int u = 0; u < min(2, U) && wait_k(u); ++u) {
+            tc::fence_after_sync();
+            issue_s(u);
+          }
           for (int u = 0; ok && u < U; ++u) {
             const int pg = page_of(u);
             if (!wait(&v_full[pg % VS], (pg / VS) & 1, kDevTimeoutFull)) break;
+            if (u + 2 < U && !wait_k(u + 2)) break;  // ahead of P: a wait costs 100 cycles even when it is over
             if (!wait(&p_full[2 * x + (u & 1)], phase >> (u & 1) & 1, kDevTimeoutSoftmax)) break;
             phase ^= 1u << (u & 1);
             tc::fence_after_sync();
@@ -329,10 +334,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
             for (int kk = 0; kk < 4; ++kk)
               tc::mma_bf16_ts(t_o(x), t_s(x, u & 1) + kk * 8, vd + ((kk * 32) >> 4), idesc_o,
                               (u > 0 || kk > 0) ? 1u : 0u);
-            free_page(&v_free[pg % VS], two);
             // the next S also says that this product is done; the last two have no next S
             if (u + 2 < U) issue_s(u + 2);
             else tc::commit(u + 1 < U ? &pv_done[x] : &o_done[x]);
+            free_page(&v_free[pg % VS], two);
           }
         }
         if (*abort_flag) break;

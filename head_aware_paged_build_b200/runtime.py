@@ -28,6 +28,11 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _current_raw_stream(index: int) -> int:
+    """Handle of device ``index``'s current stream, without building a stream object (5 us a call)."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
 class SegPagedLayer:
     """Plan + device buffers of one attention layer's batch.
 
@@ -67,7 +72,9 @@ class SegPagedLayer:
         else:
             self.k_pool, self.v_pool = pools
         self.workspace = torch.zeros(z.workspace_bytes, dtype=torch.uint8, device=self.device)
+        self.index = self.k_pool.device.index
         self.tree_workspaces: list[torch.Tensor] = []  # of tree_attention; the last is in use
+        self.tree_nodes = 0  # nodes the last of them covers
 
     # -- argument checks (the C ABI sees only pointers and strides) ------------
     def _check_tensor(self, t: torch.Tensor, what: str, dtype: torch.dtype) -> None:
@@ -188,12 +195,21 @@ class SegPagedLayer:
 
         A call makes it when it is missing; a CUDA graph capture needs it made before.  Workspaces
         that a larger one replaced are kept: a captured graph may hold their addresses."""
+        if max_nodes <= self.tree_nodes:
+            return
         need = S.segpaged_tree_workspace(self.plan, max_nodes)
-        if not self.tree_workspaces or self.tree_workspaces[-1].numel() < need:
-            if torch.cuda.is_current_stream_capturing():
-                raise RuntimeError("call prepare_tree(max_nodes) before a CUDA graph capture")
-            self.tree_workspaces.append(torch.zeros(need, dtype=torch.uint8, device=self.device))
-            torch.cuda.current_stream(self.device).synchronize()  # zeroed before any stream's call uses it
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("call prepare_tree(max_nodes) before a CUDA graph capture")
+        device = self.k_pool.device
+        self.tree_workspaces.append(torch.zeros(need, dtype=torch.uint8, device=device))
+        torch.cuda.current_stream(device).synchronize()  # zeroed before any stream's call uses it
+        self.tree_nodes = max_nodes
+
+    def _elsewhere(self, stream) -> bool:
+        """Does a call have to be made under another current device or stream?"""
+        if isinstance(stream, torch.cuda.Stream) and stream.device != self.k_pool.device:
+            raise ValueError(f"the stream is on {stream.device}, the layer's buffers on {self.k_pool.device}")
+        return stream is not None or torch.cuda.current_device() != self.index
 
     def _check_draft(self, k: torch.Tensor, v: torch.Tensor, nodes: int) -> None:
         self._check_tensor(k, "k_draft", self.torch_dtype)
@@ -229,23 +245,29 @@ class SegPagedLayer:
         self._check_index(parents, "parents", self.batch, T)
         if num_nodes is not None:
             self._check_index(num_nodes, "num_nodes", self.batch)
-        with _on(self.device, stream):  # fresh outputs and workspaces belong to the call's stream
-            fresh = torch.empty_like if num_nodes is None else torch.zeros_like
-            out = fresh(q) if out is None else out
+        if out is not None:
             self._check_tensor(out, "out", self.torch_dtype)
             if out.shape != q.shape or not out.is_contiguous():
                 raise ValueError(f"out must be contiguous {tuple(q.shape)}, got {tuple(out.shape)}")
-            lse = fresh(q[..., 0], dtype=torch.float32, memory_format=torch.contiguous_format) if lse is None else lse
+        if lse is not None:
             self._check_tensor(lse, "lse", torch.float32)
             if tuple(lse.shape) != rows or not lse.is_contiguous():
                 raise ValueError(f"lse must be contiguous {rows}, got {tuple(lse.shape)}")
-            self.prepare_tree(T)
-            ws = self.tree_workspaces[-1]
-            S.segpaged_tree_attention(self.plan, self.table.data_ptr(), self.k_pool.data_ptr(), self.v_pool.data_ptr(),
-                                      q.data_ptr(), k_draft.data_ptr(), v_draft.data_ptr(), k_draft.stride(0),
-                                      k_draft.stride(1), k_draft.stride(2), parents.data_ptr(),
-                                      num_nodes.data_ptr() if num_nodes is not None else None, T, out.data_ptr(),
-                                      lse.data_ptr(), scale, ws.data_ptr(), ws.numel(), _stream(None))
+        if self._elsewhere(stream):  # fresh outputs and workspaces belong to the call's stream
+            with _on(self.k_pool.device, stream):
+                return self.tree_attention(q, k_draft, v_draft, parents, num_nodes, out, lse, scale)
+        fresh = torch.empty if num_nodes is None else torch.zeros
+        if out is None:
+            out = fresh(q.shape, dtype=q.dtype, device=q.device)
+        if lse is None:
+            lse = fresh(rows, dtype=torch.float32, device=q.device)
+        self.prepare_tree(T)
+        ws = self.tree_workspaces[-1]
+        S.segpaged_tree_attention(self.plan, self.table.data_ptr(), self.k_pool.data_ptr(), self.v_pool.data_ptr(),
+                                  q.data_ptr(), k_draft.data_ptr(), v_draft.data_ptr(), k_draft.stride(0),
+                                  k_draft.stride(1), k_draft.stride(2), parents.data_ptr(),
+                                  num_nodes.data_ptr() if num_nodes is not None else None, T, out.data_ptr(),
+                                  lse.data_ptr(), scale, ws.data_ptr(), ws.numel(), _current_raw_stream(self.index))
         return out, lse
 
     def tree_commit(self, k_draft: torch.Tensor, v_draft: torch.Tensor, path: torch.Tensor, path_len: torch.Tensor,
@@ -261,11 +283,13 @@ class SegPagedLayer:
             raise ValueError("path must be an int32 [B, M] tensor")
         self._check_index(path, "path", self.batch, path.shape[1])
         self._check_index(path_len, "path_len", self.batch)
-        with _on(self.device, stream):
-            S.segpaged_tree_commit(self.plan, self.table.data_ptr(), k_draft.data_ptr(), v_draft.data_ptr(),
-                                   k_draft.stride(0), k_draft.stride(1), k_draft.stride(2), k_draft.shape[1],
-                                   path.data_ptr(), path_len.data_ptr(), path.shape[1], self.k_pool.data_ptr(),
-                                   self.v_pool.data_ptr(), self.workspace.data_ptr(), _stream(None))
+        if self._elsewhere(stream):
+            with _on(self.k_pool.device, stream):
+                return self.tree_commit(k_draft, v_draft, path, path_len)
+        S.segpaged_tree_commit(self.plan, self.table.data_ptr(), k_draft.data_ptr(), v_draft.data_ptr(),
+                               k_draft.stride(0), k_draft.stride(1), k_draft.stride(2), k_draft.shape[1],
+                               path.data_ptr(), path_len.data_ptr(), path.shape[1], self.k_pool.data_ptr(),
+                               self.v_pool.data_ptr(), self.workspace.data_ptr(), _current_raw_stream(self.index))
 
     def reorder(self, parents: torch.Tensor, common_len: torch.Tensor | None = None, stream=None) -> None:
         """Ring plans: sequence b goes on with the cache of sequence ``parents[b]`` (int32 [B]), in place.
@@ -275,10 +299,12 @@ class SegPagedLayer:
         self._check_index(parents, "parents", self.batch)
         if common_len is not None:
             self._check_index(common_len, "common_len", self.batch)
-        with _on(self.device, stream):
-            S.segpaged_reorder(self.plan, self.table.data_ptr(), parents.data_ptr(),
-                               common_len.data_ptr() if common_len is not None else None, self.k_pool.data_ptr(),
-                               self.v_pool.data_ptr(), self.workspace.data_ptr(), _stream(None))
+        if self._elsewhere(stream):
+            with _on(self.k_pool.device, stream):
+                return self.reorder(parents, common_len)
+        S.segpaged_reorder(self.plan, self.table.data_ptr(), parents.data_ptr(),
+                           common_len.data_ptr() if common_len is not None else None, self.k_pool.data_ptr(),
+                           self.v_pool.data_ptr(), self.workspace.data_ptr(), _current_raw_stream(self.index))
 
     def device_status(self, stream=None) -> int:
         """The first recorded code of the layer's workspaces (0: none)."""
