@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-          tc::mma_bf16_ss(ts, qd + off, kd + off, idesc_s, kk > 0);
+          tc::mma_f16_ss(ts, qd + off, kd + off, idesc_s, kk > 0);
         }
         tc::commit(&bars->s_full[x]);
       };
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
         const uint32_t to = t_o(x), ts = t_s(x);
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)  // P of page h sits at columns [64 h, 64 h + 32)
-          tc::mma_bf16_ts(to, ts + (kk >> 2) * 64 + (kk & 3) * 8, vd + (((kk >> 2) * (D * 128) + (kk & 3) * 32) >> 4),
+          tc::mma_f16_ts(to, ts + (kk >> 2) * 64 + (kk & 3) * 8, vd + (((kk >> 2) * (D * 128) + (kk & 3) * 32) >> 4),
                           idesc_o, (acc || kk > 0) ? 1u : 0u);
       };
       bool ok = mbar_wait(&bars->q, 0) && mbar_wait(&kv_full[0], 0);

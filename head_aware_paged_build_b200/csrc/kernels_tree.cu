@@ -180,6 +180,7 @@ __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 
 
   if (warp > NC) {
     // ------------------------------ draft page ------------------------------
+    constexpr DraftForm FORM = FP8 ? kDraftE4m3 : kDraftBf16;
     const bool does_k = warp == NC + 1, does_v = warp == NC + ND;
     for (int pi = 0;; ++pi) {
       const int ps = pi & 1;
@@ -191,8 +192,8 @@ __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 
         // the producer has seen the stage free (a wait on the stage's own barrier could be phases ahead of it)
         if (!__all_sync(kAll, mbar_wait(&draft_go[ps], (pi >> 1) & 1))) break;
         uint8_t* page = stage + s * 2 * PB;
-        if (does_k) tree_draft_k<D, FP8>(a, in.pc.hd, in.pc.n, page, P * 128, lane);
-        if (does_v) tree_draft_v<D, FP8>(a, in.pc.hd, in.pc.n, page + PB, lane);
+        if (does_k) tree_draft_k<D, FORM>(a, in.pc.hd, in.pc.n, page, lane);
+        if (does_v) tree_draft_v<D, FORM>(a, in.pc.hd, in.pc.n, page + PB, lane);
         fence_proxy_async_smem();  // before a later bulk copy into this stage
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[s]);
@@ -608,7 +609,7 @@ cudaError_t launch_rows(const TreeLaunch& a, cudaStream_t s) {
 TreeConfig tree_config(const sp_plan* plan, int32_t nodes) {
   const int g = plan->group, all = nodes * g;
   TreeConfig c{};
-  c.tensor = plan->prob.dtype == SP_BF16 && !plan->fp8 && all > 32;
+  c.tensor = plan->prob.dtype == SP_BF16 && all > 32;
   c.nodes_per_tile = 128 / g;
   int most;
   if (c.tensor) {

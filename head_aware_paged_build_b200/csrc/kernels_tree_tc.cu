@@ -1,5 +1,5 @@
-// Attention of a drafted tree over bf16 pages on 5th-generation tensor cores
-// (tcgen05, sm_100a): the many-row form.
+// Attention of a drafted tree on 5th-generation tensor cores (tcgen05, sm_100a):
+// the many-row form, over bf16 and E4M3 pages.
 //
 // One persistent CTA an SM walks its pieces of the work line (tree_common.cuh).
 // A query tile is up to 128 rows (nodes x the group's q-heads, TMEM lane = row),
@@ -28,8 +28,12 @@
 //              free after S, a V page only a softmax and O += P V later
 //   warps 4-7  softmax of stream 0, warps 8-11 of stream 1: a thread a row; lazy
 //              rescale of O (only when the row's maximum grows by more than 2^8), P
-//              written as bf16 over the page's own S
-// Sums, maxima and O are fp32; P is rounded to bf16, V's own type.
+//              written in 16 bits over the page's own S
+//   warps 12-15  E4M3 pages only: the codes arrive in rings of their own (warps 0, 2)
+//              and two warps each widen K and V into the operand rings, once a page,
+//              as f16, which holds every code; Q is rewritten as f16 in place
+// Sums, maxima and O are fp32; P is rounded to the operands' type: bf16, V's own, or
+// f16 over widened codes.
 // Every wait is bounded; one that runs out records a status code, and the CTA
 // drains its copies and MMAs, frees its TMEM and returns.
 #include <cuda.h>
@@ -42,8 +46,9 @@
 namespace sp {
 namespace {
 
-constexpr int kThreads = 384;
 constexpr int kSoftmaxThreads = 256;
+// E4M3 form, 512 threads: 128 registers at launch (65536); 80 x 256 + 168 x 256 = 63488.
+constexpr int kRegsMove = 80, kRegsSoftmax = 168;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.f;
 constexpr uint32_t kAll = 0xffffffffu;
@@ -54,25 +59,30 @@ constexpr uint32_t kPolyMask = 0b10000000;
 // softmax that reads the description.
 constexpr int kDescs = 16;
 
-template <int D, bool WIDE>
+template <int D, bool WIDE, bool FP8>
 struct TreeTc {
+  static constexpr int kThreads = FP8 ? 512 : 384;
   static constexpr int kQ = D / 64 * 16384;  // a query tile: [D/64][128 rows][128 B]
   static constexpr int kPage = 64 * D * 2;   // a K page [D/64][64 tokens][128 B], a V page [D rows][128 B]
+  static constexpr int kRaw = 64 * D;        // a page of codes
   static constexpr int kQTiles = WIDE ? 2 : 1;
   // the 224 KB that Q leaves, in pages: K waits for its copy alone, V for a softmax too
-  static constexpr int KS = D == 128 ? (WIDE ? 3 : 4) : 8, VS = D == 128 ? (WIDE ? 5 : 8) : 12;
+  static constexpr int KS = D == 128 ? (WIDE || FP8 ? 3 : 4) : (FP8 ? 6 : 8);
+  static constexpr int VS = D == 128 ? (FP8 ? 4 : WIDE ? 5 : 8) : (FP8 ? 8 : 12);
+  static constexpr int RS = !FP8 ? 0 : D == 128 ? (WIDE ? 3 : 5) : 6;  // pages of codes, K and V each
   static constexpr int kOffK = kQTiles * kQ;
   static constexpr int kOffV = kOffK + KS * kPage;
-  static constexpr int kOffMl = kOffV + VS * kPage;  // (m, l) of each row and stream
+  static constexpr int kOffRaw = kOffV + VS * kPage;     // K codes, then V codes
+  static constexpr int kOffMl = kOffRaw + 2 * RS * kRaw;  // (m, l) of each row and stream
   static constexpr int kOffDesc = kOffMl + 2 * 128 * 8;
   static constexpr int kOffInfo = kOffDesc + kDescs * 8;
   using Split = TreeSplit<1, 4, 6>;
   using Info = TreePieceInfo<typename Split::Piece>;
   static constexpr int kOffBar = kOffInfo + (2 * int(sizeof(Info)) + 7) / 8 * 8;
-  static constexpr int kBytes = kOffBar + (20 + 2 * KS + 2 * VS) * 8 + 8;
-  static_assert(KS + 4 <= kDescs, "page descriptions");
+  static constexpr int kBytes = kOffBar + (22 + 2 * KS + 2 * VS + 4 * RS) * 8 + 8 + 8 * (RS > 0);
+  static_assert(KS + RS + 4 <= kDescs, "page descriptions");
   static_assert(kBytes <= 232448, "shared memory of a CTA");
-  static_assert(kOffK % 1024 == 0 && kPage % 1024 == 0 && kOffMl % 8 == 0 && kOffDesc % 8 == 0 &&
+  static_assert(kOffK % 1024 == 0 && kPage % 1024 == 0 && kRaw % 1024 == 0 && kOffMl % 8 == 0 && kOffDesc % 8 == 0 &&
                     kOffInfo % alignof(Info) == 0 && kOffBar % 8 == 0,
                 "alignment of the shared-memory parts");
   static_assert((kThreads / 32 + 2) * 8 <= 2 * 128 * 8, "the split's scratch lies in the statistics' place");
@@ -87,12 +97,24 @@ struct PageSlots {
 constexpr int32_t kSlotsAll = -1;    // every row sees every slot
 constexpr int32_t kSlotsDraft = -2;  // the draft's page
 
-template <int D, bool WIDE>
-__global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, TreeLaunch a) {
-  using C = TreeTc<D, WIDE>;
+// Widen 16 codes to two 16-byte chunks of f16.
+__device__ __forceinline__ void widen16(const uint4& c, uint4& lo, uint4& hi) {
+  lo = make_uint4(e4m3x2_to_f16x2(uint16_t(c.x)), e4m3x2_to_f16x2(uint16_t(c.x >> 16)),
+                  e4m3x2_to_f16x2(uint16_t(c.y)), e4m3x2_to_f16x2(uint16_t(c.y >> 16)));
+  hi = make_uint4(e4m3x2_to_f16x2(uint16_t(c.z)), e4m3x2_to_f16x2(uint16_t(c.z >> 16)),
+                  e4m3x2_to_f16x2(uint16_t(c.w)), e4m3x2_to_f16x2(uint16_t(c.w >> 16)));
+}
+
+template <int D, bool WIDE, bool FP8>
+__global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
+    tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, TreeLaunch a) {
+  using C = TreeTc<D, WIDE, FP8>;
   using Split = typename C::Split;
   using Info = typename C::Info;
-  constexpr int KS = C::KS, VS = C::VS, kUses = WIDE ? 2 : 1;
+  constexpr int kThreads = C::kThreads;
+  constexpr int KS = C::KS, VS = C::VS, RS = C::RS, kUses = WIDE ? 2 : 1;
+  // the rings that the copies fill
+  constexpr int KR = FP8 ? RS : KS, VR = FP8 ? RS : VS, kCopy = FP8 ? C::kRaw : C::kPage;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t *k_ring = smem + C::kOffK, *v_ring = smem + C::kOffV;
   float2* ml_s = reinterpret_cast<float2*>(smem + C::kOffMl);
@@ -103,9 +125,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
   // [stream][buffer]: a softmax warp without rows may be a buffer ahead of the others, not two
   uint64_t *s_full = bars + 8, *p_full = bars + 12;
   uint64_t *pv_done = bars + 16, *o_done = bars + 18;  // a piece's last but one O += P V of a stream, and its last
-  uint64_t *k_full = bars + 20, *k_free = k_full + KS, *v_full = k_free + KS, *v_free = v_full + VS;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_free + VS);
+  uint64_t* q_ready = bars + 20;                                   // E4M3: Q is f16
+  uint64_t *k_full = bars + 22, *k_free = k_full + KS, *v_full = k_free + KS, *v_free = v_full + VS;
+  // the rings that the copies fill
+  uint8_t *kr_ring = FP8 ? smem + C::kOffRaw : k_ring, *vr_ring = FP8 ? kr_ring + RS * C::kRaw : v_ring;
+  uint64_t *kr_full = FP8 ? v_free + VS : k_full, *kr_free = FP8 ? kr_full + RS : k_free;
+  uint64_t *vr_full = FP8 ? kr_free + RS : v_full, *vr_free = FP8 ? vr_full + RS : v_free;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_free + VS + 4 * RS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int8_t* v_kind = reinterpret_cast<volatile int8_t*>(tmem_slot + 2);  // E4M3: what a place of V's codes holds
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -118,11 +146,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
       mbar_init(&pv_done[x], 1);
       mbar_init(&o_done[x], 1);
       mbar_init(&piece_full[x], 1);
-      mbar_init(&piece_free[x], 8 + 3);  // softmax warps; MMA issuers, V producer
+      mbar_init(&piece_free[x], 8 + 3 + (FP8 ? 4 : 0));  // softmax warps; MMA issuers, V producer; widening warps
     }
     // a page of two query tiles is free when both issuers' products have read it (of one: its stream's, kUses times)
-    for (int s = 0; s < KS; ++s) mbar_init(&k_full[s], 1), mbar_init(&k_free[s], kUses);
-    for (int s = 0; s < VS; ++s) mbar_init(&v_full[s], 1), mbar_init(&v_free[s], kUses);
+    for (int s = 0; s < KS; ++s) mbar_init(&k_full[s], FP8 ? 2 : 1), mbar_init(&k_free[s], kUses);
+    for (int s = 0; s < VS; ++s) mbar_init(&v_full[s], FP8 ? 2 : 1), mbar_init(&v_free[s], kUses);
+    if constexpr (FP8) {
+      mbar_init(q_ready, 2);
+      for (int s = 0; s < RS; ++s) {
+        mbar_init(&kr_full[s], 1), mbar_init(&kr_free[s], 2);
+        mbar_init(&vr_full[s], 1), mbar_init(&vr_free[s], 2);
+      }
+    }
     *abort_flag = 0;
     fence_barrier_init();
     tc::prefetch_tensormap(&qmap);
@@ -149,205 +184,291 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
   int pi = 0;  // pieces so far
   bool ok = true;
 
-  if (warp == 0 || warp == 2) {
-    // A producer's pages: records fetched 32 at a time, a lane each; kDraftPage for the draft's, kNoPage for an
-    // empty record or a page id outside the pool.
-    int4 mine = make_int4(0, 0, 0, 0);
-    auto fetch = [&](const typename Split::Piece& pc, int p) {
-      if (p + lane < min(pc.live, pc.p1))
-        mine = *reinterpret_cast<const int4*>(a.pages + pc.hd.vpage_begin + p + lane);
-    };
-    auto page = [&](const typename Split::Piece& pc, int p) {
-      const int i = (p - pc.p0) & 31;
-      if (i == 0 && p > pc.p0) fetch(pc, p);
-      const PageDesc rec{__shfl_sync(kAll, mine.x, i), __shfl_sync(kAll, mine.y, i), __shfl_sync(kAll, mine.z, i), 0};
-      if (p >= pc.live) return PageDesc{kDraftPage, 0, 0, 0};
-      if (slot_hi(rec) <= slot_lo(rec)) return PageDesc{kNoPage, 0, 0, 0};
-      if (rec.phys >= 0 && rec.phys < a.pool_pages) return rec;
-      if (lane == 0) record_error(a.status, kDevBadPage);  // corrupted table: report, read nothing there
-      return PageDesc{kNoPage, 0, 0, 0};
-    };
-    // a wait by lane 0, its outcome for the warp
-    auto wait0 = [&](uint64_t* bar, int parity, int32_t code) {
-      ok = __shfl_sync(kAll, int(lane == 0 && mbar_wait(bar, parity)), 0);
-      if (!ok && lane == 0) fail(code);
-      return ok;
-    };
-    if (warp == 0) {
-      // ------------------------------ pieces, Q and K ------------------------------
-      const uint8_t* kpool = static_cast<const uint8_t*>(a.kpool);
-      typename Split::Walk walk = split.walk();
-      typename Split::Piece pc;
-      auto slot_free = [&] { return pi < 2 || wait0(&piece_free[pi & 1], ((pi >> 1) - 1) & 1, kDevTimeoutEmpty); };
-      while (ok && split.next(a, walk, pc)) {
-        const bool two = WIDE && pc.nodes > npt;
-        fetch(pc, pc.p0);
-        if (!slot_free()) break;
-        tree_publish(a, pc, k, lane, info[pi & 1]);
-        if (lane == 0) mbar_arrive(&piece_full[pi & 1]);
-        const int p_last = pc.hd.ctx_len + pc.n - 1;
-        for (int p = pc.p0; p < pc.p1; ++p, ++k) {
-          const int st = k % KS;
-          uint8_t* k_s = k_ring + st * C::kPage;
-          const PageDesc pg = page(pc, p);
-          if (k >= KS && !wait0(&k_free[st], ((k / KS) - 1) & 1, kDevTimeoutEmpty)) break;
-          if (pg.phys == kDraftPage) {
-            tree_draft_k<D, false>(a, pc.hd, pc.n, k_s, 8192, lane);
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-          if (lane == 0) {
-            slots_s[k % kDescs] =
-                PageSlots{pg.abs_start, pg.phys == kDraftPage                                      ? kSlotsDraft
-                                        : pg.phys >= 0 && tree_page_full(pg, pc.hd, p_last) ? kSlotsAll
-                                                                                            : pg.span};
-            if (pg.phys >= 0) {
-              mbar_arrive_expect_tx(&k_full[st], C::kPage);
-              bulk_g2s(k_s, kpool + int64_t(pg.phys) * a.page_bytes, C::kPage, &k_full[st]);
-            } else {
-              mbar_arrive(&k_full[st]);
-            }
-          }
-          __syncwarp();
-          if (p == pc.p0) {  // behind the first K page: Q's place is free only after the previous piece's last S
-            if (pi > 0 && !wait0(q_free, (pi - 1) & 1, kDevTimeoutMma)) break;
-            if (lane == 0) {
-              mbar_arrive_expect_tx(q_full, (two ? 2 : 1) * (D / 64) * npt * G * 128);
-              for (int x = 0; x < (two ? 2 : 1); ++x)
-#pragma unroll
-                for (int h = 0; h < D / 64; ++h)
-                  tc::tma_load_3d(smem + x * C::kQ + h * 16384, &qmap, h * 64, pc.hd.kv * G,
-                                  pc.hd.b * a.T + pc.node0 + x * npt, q_full);
-            }
-            __syncwarp();
-            ++pi;
-          }
-        }
-      }
-      if (ok && slot_free() && lane == 0) {
-        info[pi & 1].pc.head = -1;
-        mbar_arrive(&piece_full[pi & 1]);
-      }
-      // drain: never leave with copies still writing this CTA's shared memory
-      if (lane == 0) {
-        if (pi > 0) mbar_wait(q_full, (pi - 1) & 1);
-        for (int j = (k > KS ? k - KS : 0); j < k; ++j)
-          if (!mbar_wait(&k_full[j % KS], (j / KS) & 1)) break;
-      }
-    } else {
-      // ------------------------------ V ------------------------------
-      const uint8_t* vpool = static_cast<const uint8_t*>(a.vpool);
-      for (; ok; ++pi) {
-        const int ps = pi & 1;
-        if (!wait0(&piece_full[ps], (pi >> 1) & 1, kDevTimeoutFull) || info[ps].pc.head < 0) break;
-        const typename Split::Piece pc = info[ps].pc;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&piece_free[ps]);
-        fetch(pc, pc.p0);
-        for (int p = pc.p0; p < pc.p1; ++p, ++k) {
-          const int st = k % VS;
-          uint8_t* v_s = v_ring + st * C::kPage;
-          const PageDesc pg = page(pc, p);
-          if (k >= VS && !wait0(&v_free[st], ((k / VS) - 1) & 1, kDevTimeoutEmpty)) break;
-          if (pg.phys < 0) {
-            if (pg.phys == kDraftPage) {
-              tree_draft_v<D, false>(a, pc.hd, pc.n, v_s, lane);
-            } else {  // no page: weights of zero meet values of zero
-              for (int e = lane; e < C::kPage / 16; e += 32)
-                reinterpret_cast<uint4*>(v_s)[e] = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-          if (lane == 0) {
-            if (pg.phys >= 0) {
-              mbar_arrive_expect_tx(&v_full[st], C::kPage);
-              bulk_g2s(v_s, vpool + int64_t(pg.phys) * a.page_bytes, C::kPage, &v_full[st]);
-            } else {
-              mbar_arrive(&v_full[st]);
-            }
-          }
-          __syncwarp();
-        }
-      }
-      if (lane == 0)
-        for (int j = (k > VS ? k - VS : 0); j < k; ++j)
-          if (!mbar_wait(&v_full[j % VS], (j / VS) & 1)) break;
-    }
-  } else if (warp < 4) {
-    if (lane == 0) {
-      // ------------------------------ MMA issuers ------------------------------
-      const int x = warp >> 1;  // stream
-      constexpr uint32_t idesc_s = tc::idesc_bf16_f32(128, 64);
-      constexpr uint32_t idesc_o = tc::idesc_bf16_f32(128, D);
-      const uint32_t q_addr = smem_u32(smem), k_addr = smem_u32(k_ring), v_addr = smem_u32(v_ring);
-      uint32_t phase = 0;  // bit b: parity of the phase of the stream's P buffer b
-      auto wait = [&](uint64_t* bar, int parity, int32_t code) {
-        ok = mbar_wait(bar, parity);
-        if (!ok) fail(code);
+  if (warp < 4) {
+    if constexpr (FP8) tc::reg_dealloc<kRegsMove>();
+    if (warp == 0 || warp == 2) {
+      // A producer's pages: records fetched 32 at a time, a lane each; kDraftPage for the draft's, kNoPage for an
+      // empty record or a page id outside the pool.
+      int4 mine = make_int4(0, 0, 0, 0);
+      auto fetch = [&](const typename Split::Piece& pc, int p) {
+        if (p + lane < min(pc.live, pc.p1))
+          mine = *reinterpret_cast<const int4*>(a.pages + pc.hd.vpage_begin + p + lane);
+      };
+      auto page = [&](const typename Split::Piece& pc, int p) {
+        const int i = (p - pc.p0) & 31;
+        if (i == 0 && p > pc.p0) fetch(pc, p);
+        const PageDesc rec{__shfl_sync(kAll, mine.x, i), __shfl_sync(kAll, mine.y, i), __shfl_sync(kAll, mine.z, i), 0};
+        if (p >= pc.live) return PageDesc{kDraftPage, 0, 0, 0};
+        if (slot_hi(rec) <= slot_lo(rec)) return PageDesc{kNoPage, 0, 0, 0};
+        if (rec.phys >= 0 && rec.phys < a.pool_pages) return rec;
+        if (lane == 0) record_error(a.status, kDevBadPage);  // corrupted table: report, read nothing there
+        return PageDesc{kNoPage, 0, 0, 0};
+      };
+      // a wait by lane 0, its outcome for the warp
+      auto wait0 = [&](uint64_t* bar, int parity, int32_t code) {
+        ok = __shfl_sync(kAll, int(lane == 0 && mbar_wait(bar, parity)), 0);
+        if (!ok && lane == 0) fail(code);
         return ok;
       };
-      // the stream's last product of a page is issued: its place is free when that has run
-      auto free_page = [&](uint64_t* bar, bool two) {
-        tc::commit(bar);
-        if (WIDE && !two) tc::commit(bar);
-      };
-      while (ok) {
-        const int ps = pi & 1;
-        if (!wait(&piece_full[ps], (pi >> 1) & 1, kDevTimeoutFull) || info[ps].pc.head < 0) break;
-        const bool two = WIDE && info[ps].pc.nodes > npt;
-        const int np = info[ps].pc.p1 - info[ps].pc.p0, U = two ? np : (np + 1 - x) / 2;
-        mbar_arrive(&piece_free[ps]);
-        auto page_of = [&](int u) { return k + (two ? u : 2 * u + x); };
-        const uint64_t qd = tc::smem_desc_sw128(q_addr + (two ? x : 0) * C::kQ);
-        auto wait_k = [&](int u) {
-          const int pg = page_of(u);
-          return wait(&k_full[pg % KS], (pg / KS) & 1, kDevTimeoutFull);
-        };
-        auto issue_s = [&](int u) {
-          const int pg = page_of(u);
-          const uint64_t kd = tc::smem_desc_sw128(k_addr + (pg % KS) * C::kPage);
+      if (warp == 0) {
+        // ------------------------------ pieces, Q and K ------------------------------
+        const uint8_t* kpool = static_cast<const uint8_t*>(a.kpool);
+        typename Split::Walk walk = split.walk();
+        typename Split::Piece pc;
+        auto slot_free = [&] { return pi < 2 || wait0(&piece_free[pi & 1], ((pi >> 1) - 1) & 1, kDevTimeoutEmpty); };
+        while (ok && split.next(a, walk, pc)) {
+          const bool two = WIDE && pc.nodes > npt;
+          fetch(pc, pc.p0);
+          if (!slot_free()) break;
+          tree_publish(a, pc, k, lane, info[pi & 1]);
+          if (lane == 0) mbar_arrive(&piece_full[pi & 1]);
+          const int p_last = pc.hd.ctx_len + pc.n - 1;
+          for (int p = pc.p0; p < pc.p1; ++p, ++k) {
+            const int st = k % KR;
+            uint8_t* k_s = kr_ring + st * kCopy;
+            const PageDesc pg = page(pc, p);
+            if (k >= KR && !wait0(&kr_free[st], ((k / KR) - 1) & 1, kDevTimeoutEmpty)) break;
+            if (!FP8 && pg.phys == kDraftPage) {
+              tree_draft_k<D, kDraftBf16>(a, pc.hd, pc.n, k_s, lane);
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+            if (lane == 0) {
+              slots_s[k % kDescs] =
+                  PageSlots{pg.abs_start, pg.phys == kDraftPage                                      ? kSlotsDraft
+                                          : pg.phys >= 0 && tree_page_full(pg, pc.hd, p_last) ? kSlotsAll
+                                                                                              : pg.span};
+              if (pg.phys >= 0) {
+                mbar_arrive_expect_tx(&kr_full[st], kCopy);
+                bulk_g2s(k_s, kpool + int64_t(pg.phys) * a.page_bytes, kCopy, &kr_full[st]);
+              } else {
+                mbar_arrive(&kr_full[st]);
+              }
+            }
+            __syncwarp();
+            if (p == pc.p0) {  // behind the first K page: Q's place is free only after the previous piece's last S
+              if (pi > 0 && !wait0(q_free, (pi - 1) & 1, kDevTimeoutMma)) break;
+              if (lane == 0) {
+                mbar_arrive_expect_tx(q_full, (two ? 2 : 1) * (D / 64) * npt * G * 128);
+                for (int x = 0; x < (two ? 2 : 1); ++x)
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            tc::mma_bf16_ss(t_s(x, u & 1), qd + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
-                            kd + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
-          tc::commit(&s_full[2 * x + (u & 1)]);
-          free_page(&k_free[pg % KS], two);
-          if (u == U - 1) tc::commit(q_free);
-        };
-        if (U == 0) {  // a piece of one page
-          mbar_arrive(q_free);
-        } else if (wait(q_full, pi & 1, kDevTimeoutFull)) {
-          for (int u = 0; u < min(2, U) && wait_k(u); ++u) {
-            tc::fence_after_sync();
-            issue_s(u);
-          }
-          for (int u = 0; ok && u < U; ++u) {
-            const int pg = page_of(u);
-            if (!wait(&v_full[pg % VS], (pg / VS) & 1, kDevTimeoutFull)) break;
-            if (u + 2 < U && !wait_k(u + 2)) break;  // ahead of P: a wait costs 100 cycles even when it is over
-            if (!wait(&p_full[2 * x + (u & 1)], phase >> (u & 1) & 1, kDevTimeoutSoftmax)) break;
-            phase ^= 1u << (u & 1);
-            tc::fence_after_sync();
-            const uint64_t vd = tc::smem_desc_sw128(v_addr + (pg % VS) * C::kPage);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc::mma_bf16_ts(t_o(x), t_s(x, u & 1) + kk * 8, vd + ((kk * 32) >> 4), idesc_o,
-                              (u > 0 || kk > 0) ? 1u : 0u);
-            // the next S also says that this product is done; the last two have no next S
-            if (u + 2 < U) issue_s(u + 2);
-            else tc::commit(u + 1 < U ? &pv_done[x] : &o_done[x]);
-            free_page(&v_free[pg % VS], two);
+                  for (int h = 0; h < D / 64; ++h)
+                    tc::tma_load_3d(smem + x * C::kQ + h * 16384, &qmap, h * 64, pc.hd.kv * G,
+                                    pc.hd.b * a.T + pc.node0 + x * npt, q_full);
+              }
+              __syncwarp();
+              ++pi;
+            }
           }
         }
-        if (*abort_flag) break;
-        k += np, ++pi;
+        if (ok && slot_free() && lane == 0) {
+          info[pi & 1].pc.head = -1;
+          mbar_arrive(&piece_full[pi & 1]);
+        }
+        // drain: never leave with copies still writing this CTA's shared memory
+        if (lane == 0) {
+          if (pi > 0) mbar_wait(q_full, (pi - 1) & 1);
+          for (int j = (k > KR ? k - KR : 0); j < k; ++j)
+            if (!mbar_wait(&kr_full[j % KR], (j / KR) & 1)) break;
+        }
+      } else {
+        // ------------------------------ V ------------------------------
+        const uint8_t* vpool = static_cast<const uint8_t*>(a.vpool);
+        for (; ok; ++pi) {
+          const int ps = pi & 1;
+          if (!wait0(&piece_full[ps], (pi >> 1) & 1, kDevTimeoutFull) || info[ps].pc.head < 0) break;
+          const typename Split::Piece pc = info[ps].pc;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&piece_free[ps]);
+          fetch(pc, pc.p0);
+          for (int p = pc.p0; p < pc.p1; ++p, ++k) {
+            const int st = k % VR;
+            uint8_t* v_s = vr_ring + st * kCopy;
+            const PageDesc pg = page(pc, p);
+            if (k >= VR && !wait0(&vr_free[st], ((k / VR) - 1) & 1, kDevTimeoutEmpty)) break;
+            if (!FP8 && pg.phys < 0) {
+              if (pg.phys == kDraftPage) {
+                tree_draft_v<D, kDraftBf16>(a, pc.hd, pc.n, v_s, lane);
+              } else {  // no page: weights of zero meet values of zero
+                for (int e = lane; e < C::kPage / 16; e += 32)
+                  reinterpret_cast<uint4*>(v_s)[e] = make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+            if (lane == 0) {
+              if (FP8) v_kind[st] = int8_t(min(pg.phys, 0));
+              if (pg.phys >= 0) {
+                mbar_arrive_expect_tx(&vr_full[st], kCopy);
+                bulk_g2s(v_s, vpool + int64_t(pg.phys) * a.page_bytes, kCopy, &vr_full[st]);
+              } else {
+                mbar_arrive(&vr_full[st]);
+              }
+            }
+            __syncwarp();
+          }
+        }
+        if (lane == 0)
+          for (int j = (k > VR ? k - VR : 0); j < k; ++j)
+            if (!mbar_wait(&vr_full[j % VR], (j / VR) & 1)) break;
       }
-      // all MMAs issued by this thread complete before TMEM is released
-      tc::commit(&done[x]);
-      mbar_wait(&done[x], 0);
+    } else {
+      if (lane == 0) {
+        // ------------------------------ MMA issuers ------------------------------
+        const int x = warp >> 1;  // stream
+        constexpr uint32_t idesc_s = FP8 ? tc::idesc_f16_f32(128, 64) : tc::idesc_bf16_f32(128, 64);
+        constexpr uint32_t idesc_o = FP8 ? tc::idesc_f16_f32(128, D) : tc::idesc_bf16_f32(128, D);
+        const uint32_t q_addr = smem_u32(smem), k_addr = smem_u32(k_ring), v_addr = smem_u32(v_ring);
+        uint32_t phase = 0;  // bit b: parity of the phase of the stream's P buffer b
+        auto wait = [&](uint64_t* bar, int parity, int32_t code) {
+          ok = mbar_wait(bar, parity);
+          if (!ok) fail(code);
+          return ok;
+        };
+        // the stream's last product of a page is issued: its place is free when that has run
+        auto free_page = [&](uint64_t* bar, bool two) {
+          tc::commit(bar);
+          if (WIDE && !two) tc::commit(bar);
+        };
+        while (ok) {
+          const int ps = pi & 1;
+          if (!wait(&piece_full[ps], (pi >> 1) & 1, kDevTimeoutFull) || info[ps].pc.head < 0) break;
+          const bool two = WIDE && info[ps].pc.nodes > npt;
+          const int np = info[ps].pc.p1 - info[ps].pc.p0, U = two ? np : (np + 1 - x) / 2;
+          mbar_arrive(&piece_free[ps]);
+          auto page_of = [&](int u) { return k + (two ? u : 2 * u + x); };
+          const uint64_t qd = tc::smem_desc_sw128(q_addr + (two ? x : 0) * C::kQ);
+          auto wait_k = [&](int u) {
+            const int pg = page_of(u);
+            return wait(&k_full[pg % KS], (pg / KS) & 1, kDevTimeoutFull);
+          };
+          auto issue_s = [&](int u) {
+            const int pg = page_of(u);
+            const uint64_t kd = tc::smem_desc_sw128(k_addr + (pg % KS) * C::kPage);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc::mma_f16_ss(t_s(x, u & 1), qd + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                              kd + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
+            tc::commit(&s_full[2 * x + (u & 1)]);
+            free_page(&k_free[pg % KS], two);
+            if (u == U - 1) tc::commit(q_free);
+          };
+          // (waited for even without a page: a wait left out would leave the next one a phase ahead)
+          if (!wait(FP8 ? q_ready : q_full, pi & 1, kDevTimeoutFull)) break;
+          if (U == 0) {  // a piece of one page
+            mbar_arrive(q_free);
+          } else {
+            for (int u = 0; u < min(2, U) && wait_k(u); ++u) {
+              tc::fence_after_sync();
+              issue_s(u);
+            }
+            for (int u = 0; ok && u < U; ++u) {
+              const int pg = page_of(u);
+              if (!wait(&v_full[pg % VS], (pg / VS) & 1, kDevTimeoutFull)) break;
+              if (u + 2 < U && !wait_k(u + 2)) break;  // ahead of P: a wait costs 100 cycles even when it is over
+              if (!wait(&p_full[2 * x + (u & 1)], phase >> (u & 1) & 1, kDevTimeoutSoftmax)) break;
+              phase ^= 1u << (u & 1);
+              tc::fence_after_sync();
+              const uint64_t vd = tc::smem_desc_sw128(v_addr + (pg % VS) * C::kPage);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                tc::mma_f16_ts(t_o(x), t_s(x, u & 1) + kk * 8, vd + ((kk * 32) >> 4), idesc_o,
+                                (u > 0 || kk > 0) ? 1u : 0u);
+              // the next S also says that this product is done; the last two have no next S
+              if (u + 2 < U) issue_s(u + 2);
+              else tc::commit(u + 1 < U ? &pv_done[x] : &o_done[x]);
+              free_page(&v_free[pg % VS], two);
+            }
+          }
+          if (*abort_flag) break;
+          k += np, ++pi;
+        }
+        // all MMAs issued by this thread complete before TMEM is released
+        tc::commit(&done[x]);
+        mbar_wait(&done[x], 0);
+      }
+    }
+  } else if (FP8 && warp >= 12) {
+    if constexpr (FP8) {
+      // ------------------------------ widening ------------------------------
+      tc::reg_dealloc<kRegsMove>();
+      const bool is_k = warp < 14;
+      const int half = warp & 1;
+      uint8_t *raw = is_k ? kr_ring : vr_ring, *wide = is_k ? k_ring : v_ring;
+      uint64_t *raw_full = is_k ? kr_full : vr_full, *raw_free = is_k ? kr_free : vr_free;
+      uint64_t *wide_full = is_k ? k_full : v_full, *wide_free = is_k ? k_free : v_free;
+      const int WS = is_k ? KS : VS;
+      auto wait = [&](uint64_t* bar, int parity) {
+        ok = __all_sync(kAll, mbar_wait(bar, parity));
+        if (!ok) fail(kDevTimeoutFull);
+        return ok;
+      };
+      for (; ok; ++pi) {
+        const int ps = pi & 1;
+        if (!wait(&piece_full[ps], (pi >> 1) & 1)) break;
+        const Info& in = info[ps];
+        if (in.pc.head < 0) break;
+        if (!is_k) {  // Q to f16, in place: the same swizzled chunks
+          if (!wait(q_full, pi & 1)) break;
+          const int bytes = (WIDE && in.pc.nodes > npt ? 2 : 1) * C::kQ;
+#pragma unroll 4
+          for (int e = half * 32 + lane; e < bytes / 16; e += 64) {
+            uint4* q = reinterpret_cast<uint4*>(smem) + e;
+            const uint4 v = *q;
+            *q = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(q_ready);
+        }
+        const int np = in.pc.p1 - in.pc.p0;
+        for (int j = 0; j < np; ++j, ++k) {
+          const int rs = k % RS, ws = k % WS;
+          if (!wait(&raw_full[rs], (k / RS) & 1)) break;
+          if (k >= WS && !wait(&wide_free[ws], ((k / WS) - 1) & 1)) break;
+          const uint8_t* src = raw + rs * C::kRaw;
+          uint8_t* dst = wide + ws * C::kPage;
+          const int kind = is_k ? (slots_s[k % kDescs].span == kSlotsDraft ? kDraftPage : 0) : v_kind[rs];
+          if (kind == kDraftPage) {
+            if (half == 0) {
+              if (is_k) tree_draft_k<D, kDraftWide>(a, in.pc.hd, in.pc.n, dst, lane);
+              else tree_draft_v<D, kDraftWide>(a, in.pc.hd, in.pc.n, dst, lane);
+            }
+          } else if (kind == kNoPage) {  // V: weights of zero meet values of zero
+            for (int e = half * 32 + lane; e < C::kPage / 16; e += 64)
+              reinterpret_cast<uint4*>(dst)[e] = make_uint4(0, 0, 0, 0);
+          } else {
+            constexpr int UNITS = C::kRaw / 16 / 64;  // 16-code units of a lane
+#pragma unroll
+            for (int u = 0; u < UNITS; ++u) {
+              const int e = (u * 2 + half) * 32 + lane;
+              uint4 lo, hi;
+              if (is_k) {
+                const int t = e & 63, c = e >> 6;  // token, 16 dimensions
+                widen16(*reinterpret_cast<const uint4*>(src + fp8_kpage_offset(t, c * 16, D)), lo, hi);
+                *reinterpret_cast<uint4*>(dst + kpage_chunk_offset_bf16(t, 2 * c, 64)) = lo;
+                *reinterpret_cast<uint4*>(dst + kpage_chunk_offset_bf16(t, 2 * c + 1, 64)) = hi;
+              } else {
+                const int i = e % D, g = e / D;  // dimension, 16 positions
+                widen16(*reinterpret_cast<const uint4*>(src + fp8_vpage_offset(i, g * 16)), lo, hi);
+                *reinterpret_cast<uint4*>(dst + vpage_chunk_offset_bf16(i, 2 * g)) = lo;
+                *reinterpret_cast<uint4*>(dst + vpage_chunk_offset_bf16(i, 2 * g + 1)) = hi;
+              }
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&wide_full[ws]);
+            mbar_arrive(&raw_free[rs]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&piece_free[ps]);
+      }
     }
   } else {
+    if constexpr (FP8) tc::reg_alloc<kRegsSoftmax>();
     // ------------------------------ softmax ------------------------------
     const int x = (warp - 4) >> 2;
     const int quarter = warp & 3;  // TMEM lane quarter this warp may access
@@ -449,7 +570,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
               e0 = fast_exp2(x0), e1 = fast_exp2(x1);
             }
             s2[e & 1] = f2_add(s2[e & 1], f2_pack(e0, e1));
-            pk[e] = pack_bf16x2(e0, e1);
+            // E4M3: the order of the page's positions (pairs 0 4 1 5 2 6 3 7 of every 16 tokens)
+            if constexpr (FP8) pk[(e & 8) | (e & 3) << 1 | (e >> 2 & 1)] = pack_f16x2(e0, e1);
+            else pk[e] = pack_bf16x2(e0, e1);
           }
           tc::tmem_st16(ts + 16 * c, pk);
         }
@@ -561,26 +684,31 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
   }
 }
 
-template <int D, bool WIDE>
+template <int D, bool WIDE, bool FP8>
 cudaError_t launch(const TreeLaunch& a, int64_t total_rows, cudaStream_t s) {
-  using C = TreeTc<D, WIDE>;
+  using C = TreeTc<D, WIDE, FP8>;
   CUtensorMap qmap;
   cudaError_t e = encode_query_map(&qmap, a.q, D, a.num_q_heads, total_rows, a.group, a.nodes_per_tile);
   if (e != cudaSuccess) return e;
-  auto kern = tree_tc_kernel<D, WIDE>;
+  auto kern = tree_tc_kernel<D, WIDE, FP8>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
   if (e != cudaSuccess) return e;
-  kern<<<a.n_ctas, kThreads, C::kBytes, s>>>(qmap, a);
+  kern<<<a.n_ctas, C::kThreads, C::kBytes, s>>>(qmap, a);
   return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_form(const TreeLaunch& a, cudaStream_t s) {
+  const int64_t total_rows = int64_t(a.n_heads / a.num_kv_heads) * a.T;
+  const bool wide = a.nodes_per_group > a.nodes_per_tile;
+  if (a.fp8) return wide ? launch<D, true, true>(a, total_rows, s) : launch<D, false, true>(a, total_rows, s);
+  return wide ? launch<D, true, false>(a, total_rows, s) : launch<D, false, false>(a, total_rows, s);
 }
 
 }  // namespace
 
 cudaError_t launch_tree_tc(const TreeLaunch& a, cudaStream_t s) {
-  const int64_t total_rows = int64_t(a.n_heads / a.num_kv_heads) * a.T;
-  const bool wide = a.nodes_per_group > a.nodes_per_tile;
-  if (a.D == 128) return wide ? launch<128, true>(a, total_rows, s) : launch<128, false>(a, total_rows, s);
-  return wide ? launch<64, true>(a, total_rows, s) : launch<64, false>(a, total_rows, s);
+  return a.D == 128 ? launch_form<128>(a, s) : launch_form<64>(a, s);
 }
 
 }  // namespace sp

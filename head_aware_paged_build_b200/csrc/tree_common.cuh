@@ -106,15 +106,18 @@ __device__ __forceinline__ uint64_t tree_visible(uint64_t mask, const HeadDesc& 
   return mask & ~hidden;
 }
 
-// The draft's n rows as a page of 64 slots in shared memory, as an append lays
-// them out; one warp each for K (in blocks of 64 dimensions k_block bytes apart;
-// E4M3 pages are one block) and V (transposed).  Slots behind n hold zeros in V
+// Forms of the draft's page: as an append lays out bf16 and E4M3 pages, and the
+// E4M3 codes widened to f16 in the bf16 pages' layout (V's tokens in the order
+// of the E4M3 pages' positions).
+enum DraftForm { kDraftBf16, kDraftE4m3, kDraftWide };
+
+// The draft's n rows as a page of 64 slots in shared memory; one warp each for K
+// and V (transposed).  Slots behind n hold zeros in V
 // (their weights are zero, and 0 x garbage must stay 0) and are left as they are
 // in K (their scores are masked).  Loads go out in batches: the rows come from
 // global memory, and one row at a time would cost its latency up to 64 times.
-template <int D, bool FP8>
-__device__ __forceinline__ void tree_draft_k(const TreeLaunch& a, const HeadDesc& hd, int n, uint8_t* kdst,
-                                             int k_block, int lane) {
+template <int D, DraftForm FORM>
+__device__ __forceinline__ void tree_draft_k(const TreeLaunch& a, const HeadDesc& hd, int n, uint8_t* kdst, int lane) {
   const __nv_bfloat16* kn =
       static_cast<const __nv_bfloat16*>(a.k_draft) + int64_t(hd.b) * a.ds_seq + int64_t(hd.kv) * a.ds_head;
   constexpr int CR = D / 8, KB = 8;  // 16-byte chunks of a K row; loads in flight
@@ -129,30 +132,30 @@ __device__ __forceinline__ void tree_draft_k(const TreeLaunch& a, const HeadDesc
     for (int i = 0; i < KB; ++i) {
       const int u = u0 + 32 * i, t = u / CR, c = u % CR;
       if (u >= n * CR) continue;
-      if constexpr (FP8) {
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-        uint32_t q[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t lo = w[2 * h], hi = w[2 * h + 1];
-          q[h] = uint32_t(pack_e4m3x2(__uint_as_float(lo << 16) * a.k_inv,
-                                      __uint_as_float(lo & 0xffff0000u) * a.k_inv)) |
-                 uint32_t(pack_e4m3x2(__uint_as_float(hi << 16) * a.k_inv,
-                                      __uint_as_float(hi & 0xffff0000u) * a.k_inv))
-                     << 16;
-        }
-        *reinterpret_cast<uint2*>(kdst + fp8_kpage_offset(t, c * 8, D)) = make_uint2(q[0], q[1]);
+      if constexpr (FORM == kDraftBf16) {
+        *reinterpret_cast<uint4*>(kdst + kpage_chunk_offset_bf16(t, c, 64)) = v[i];
       } else {
-        *reinterpret_cast<uint4*>(kdst + (c >> 3) * k_block + t * 128 + (((c & 7) ^ (t & 7)) << 4)) = v[i];
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        uint16_t q[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+          q[h] = pack_e4m3x2(__uint_as_float(w[h] << 16) * a.k_inv, __uint_as_float(w[h] & 0xffff0000u) * a.k_inv);
+        if constexpr (FORM == kDraftE4m3)
+          *reinterpret_cast<uint2*>(kdst + fp8_kpage_offset(t, c * 8, D)) =
+              make_uint2(uint32_t(q[0]) | uint32_t(q[1]) << 16, uint32_t(q[2]) | uint32_t(q[3]) << 16);
+        else
+          *reinterpret_cast<uint4*>(kdst + kpage_chunk_offset_bf16(t, c, 64)) = make_uint4(
+              e4m3x2_to_f16x2(q[0]), e4m3x2_to_f16x2(q[1]), e4m3x2_to_f16x2(q[2]), e4m3x2_to_f16x2(q[3]));
       }
     }
   }
 }
-template <int D, bool FP8>
+template <int D, DraftForm FORM>
 __device__ __forceinline__ void tree_draft_v(const TreeLaunch& a, const HeadDesc& hd, int n, uint8_t* vdst, int lane) {
   const __nv_bfloat16* vn =
       static_cast<const __nv_bfloat16*>(a.v_draft) + int64_t(hd.b) * a.ds_seq + int64_t(hd.kv) * a.ds_head;
   // a lane takes two dimensions of a run of tokens and writes a 16-byte chunk of each
+  constexpr bool FP8 = FORM != kDraftBf16;
   constexpr int DP = D / 2, TG = FP8 ? 16 : 8;
 #pragma unroll 2
   for (int u = lane; u < DP * (64 / TG); u += 32) {
@@ -183,10 +186,20 @@ __device__ __forceinline__ void tree_draft_v(const TreeLaunch& a, const HeadDesc
         hi[w] = __byte_perm(x[2 * w], x[2 * w + 1], 0x7632);
       }
     }
-    const int64_t o0 = FP8 ? fp8_vpage_offset(i, g * 16) : vpage_chunk_offset_bf16(i, g);
-    const int64_t o1 = FP8 ? fp8_vpage_offset(i + 1, g * 16) : vpage_chunk_offset_bf16(i + 1, g);
-    *reinterpret_cast<uint4*>(vdst + o0) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    *reinterpret_cast<uint4*>(vdst + o1) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const uint32_t(&w)[4] = y ? hi : lo;
+      if constexpr (FORM == kDraftWide) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          *reinterpret_cast<uint4*>(vdst + vpage_chunk_offset_bf16(i + y, 2 * g + c)) =
+              make_uint4(e4m3x2_to_f16x2(uint16_t(w[2 * c])), e4m3x2_to_f16x2(uint16_t(w[2 * c] >> 16)),
+                         e4m3x2_to_f16x2(uint16_t(w[2 * c + 1])), e4m3x2_to_f16x2(uint16_t(w[2 * c + 1] >> 16)));
+      } else {
+        const int64_t at = FP8 ? fp8_vpage_offset(i + y, g * 16) : vpage_chunk_offset_bf16(i + y, g);
+        *reinterpret_cast<uint4*>(vdst + at) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
   }
 }
 
