@@ -76,6 +76,16 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
 }
@@ -121,6 +131,7 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
 // Bounded wait: ~2 s of wall time, then give up (returns false).  The fast
 // path is one try_wait; the slow path re-checks the clock every 256 tries.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr uint32_t kParkNs = 100000;
 
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -132,6 +143,24 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
       __nanosleep(64);
     }
   }
+}
+
+// Same, parked: a try may hold the thread back for up to `hint` ns, so that waiting warps poll rarely.
+__device__ __forceinline__ bool mbar_wait_parked(uint64_t* bar, uint32_t parity) {
+  auto try_parked = [&] {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(kParkNs)
+        : "memory");
+    return ok != 0;
+  };
+  if (try_parked()) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!try_parked())
+    if (global_timer_ns() - t0 > kWaitLimitNs) return false;
+  return true;
 }
 
 // Generic-proxy shared-memory writes -> visible to the async proxy (bulk copies, tensor cores).

@@ -52,8 +52,6 @@ constexpr int kRegsMove = 80, kRegsSoftmax = 168;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.f;
 constexpr uint32_t kAll = 0xffffffffu;
-// Exponent pairs (of every eight) computed on the FMA pipe, next to the SFU's.
-constexpr uint32_t kPolyMask = 0b10000000;
 // Page descriptions in flight: a K page's place is free once its S is made, so
 // the producer is at most KS pages ahead of S, and S four pages ahead of the
 // softmax that reads the description.
@@ -97,12 +95,29 @@ struct PageSlots {
 constexpr int32_t kSlotsAll = -1;    // every row sees every slot
 constexpr int32_t kSlotsDraft = -2;  // the draft's page
 
-// Widen 16 codes to two 16-byte chunks of f16.
-__device__ __forceinline__ void widen16(const uint4& c, uint4& lo, uint4& hi) {
-  lo = make_uint4(e4m3x2_to_f16x2(uint16_t(c.x)), e4m3x2_to_f16x2(uint16_t(c.x >> 16)),
-                  e4m3x2_to_f16x2(uint16_t(c.y)), e4m3x2_to_f16x2(uint16_t(c.y >> 16)));
-  hi = make_uint4(e4m3x2_to_f16x2(uint16_t(c.z)), e4m3x2_to_f16x2(uint16_t(c.z >> 16)),
-                  e4m3x2_to_f16x2(uint16_t(c.w)), e4m3x2_to_f16x2(uint16_t(c.w >> 16)));
+// Half a page of codes to f16, by one warp.  K: a lane is a token, a step 16
+// dimensions; V: a lane is a dimension (of 64), a step 16 positions or the next
+// 64 dimensions.  Both layouts swizzle by XOR, so a step's address is an XOR of
+// the lane's first one.  Four steps at a time in a rolled loop: all unrolled,
+// the roles' loops outgrow the instruction cache (315 us where this takes @@).
+template <int D, bool K>
+__device__ __forceinline__ void widen_page(uint32_t from, uint32_t to) {
+  constexpr bool kHalves = D == 128 && !K;  // dimensions 64 ... 127 as every other step
+#pragma unroll 1
+  for (int i0 = 0; i0 < D / 16; i0 += 4) {
+    uint4 c[4], o[2];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      c[u] = lds128(kHalves ? (from ^ ((i0 / 2 + u / 2) << 4)) + u % 2 * 4096 : from ^ ((i0 + u) << 4));
+    const uint32_t at = K ? to + i0 / 4 * 8192 : to ^ (i0 << 4);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      widen16(c[u], o[0], o[1]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        sts128(kHalves ? (at ^ ((u / 2 * 2 + h) << 4)) + u % 2 * 8192 : at ^ ((2 * u + h) << 4), o[h]);
+    }
+  }
 }
 
 template <int D, bool WIDE, bool FP8>
@@ -206,7 +221,7 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
       };
       // a wait by lane 0, its outcome for the warp
       auto wait0 = [&](uint64_t* bar, int parity, int32_t code) {
-        ok = __shfl_sync(kAll, int(lane == 0 && mbar_wait(bar, parity)), 0);
+        ok = __shfl_sync(kAll, int(lane == 0 && mbar_wait_parked(bar, parity)), 0);
         if (!ok && lane == 0) fail(code);
         return ok;
       };
@@ -267,9 +282,9 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
         }
         // drain: never leave with copies still writing this CTA's shared memory
         if (lane == 0) {
-          if (pi > 0) mbar_wait(q_full, (pi - 1) & 1);
+          if (pi > 0) mbar_wait_parked(q_full, (pi - 1) & 1);
           for (int j = (k > KR ? k - KR : 0); j < k; ++j)
-            if (!mbar_wait(&kr_full[j % KR], (j / KR) & 1)) break;
+            if (!mbar_wait_parked(&kr_full[j % KR], (j / KR) & 1)) break;
         }
       } else {
         // ------------------------------ V ------------------------------
@@ -310,7 +325,7 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
         }
         if (lane == 0)
           for (int j = (k > VR ? k - VR : 0); j < k; ++j)
-            if (!mbar_wait(&vr_full[j % VR], (j / VR) & 1)) break;
+            if (!mbar_wait_parked(&vr_full[j % VR], (j / VR) & 1)) break;
       }
     } else {
       if (lane == 0) {
@@ -321,7 +336,7 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
         const uint32_t q_addr = smem_u32(smem), k_addr = smem_u32(k_ring), v_addr = smem_u32(v_ring);
         uint32_t phase = 0;  // bit b: parity of the phase of the stream's P buffer b
         auto wait = [&](uint64_t* bar, int parity, int32_t code) {
-          ok = mbar_wait(bar, parity);
+          ok = mbar_wait_parked(bar, parity);
           if (!ok) fail(code);
           return ok;
         };
@@ -385,7 +400,7 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
         }
         // all MMAs issued by this thread complete before TMEM is released
         tc::commit(&done[x]);
-        mbar_wait(&done[x], 0);
+        mbar_wait_parked(&done[x], 0);
       }
     }
   } else if (FP8 && warp >= 12) {
@@ -398,8 +413,10 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
       uint64_t *raw_full = is_k ? kr_full : vr_full, *raw_free = is_k ? kr_free : vr_free;
       uint64_t *wide_full = is_k ? k_full : v_full, *wide_free = is_k ? k_free : v_free;
       const int WS = is_k ? KS : VS;
+      const int id = half * 32 + lane;
+      const int from0 = is_k ? fp8_kpage_offset(id, 0, D) : fp8_vpage_offset(id, 0), to0 = id * 128 + ((id & 7) << 4);
       auto wait = [&](uint64_t* bar, int parity) {
-        ok = __all_sync(kAll, mbar_wait(bar, parity));
+        ok = __all_sync(kAll, mbar_wait_parked(bar, parity));
         if (!ok) fail(kDevTimeoutFull);
         return ok;
       };
@@ -415,7 +432,7 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
           for (int e = half * 32 + lane; e < bytes / 16; e += 64) {
             uint4* q = reinterpret_cast<uint4*>(smem) + e;
             const uint4 v = *q;
-            *q = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
+  *q = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -438,23 +455,9 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
             for (int e = half * 32 + lane; e < C::kPage / 16; e += 64)
               reinterpret_cast<uint4*>(dst)[e] = make_uint4(0, 0, 0, 0);
           } else {
-            constexpr int UNITS = C::kRaw / 16 / 64;  // 16-code units of a lane
-#pragma unroll
-            for (int u = 0; u < UNITS; ++u) {
-              const int e = (u * 2 + half) * 32 + lane;
-              uint4 lo, hi;
-              if (is_k) {
-                const int t = e & 63, c = e >> 6;  // token, 16 dimensions
-                widen16(*reinterpret_cast<const uint4*>(src + fp8_kpage_offset(t, c * 16, D)), lo, hi);
-                *reinterpret_cast<uint4*>(dst + kpage_chunk_offset_bf16(t, 2 * c, 64)) = lo;
-                *reinterpret_cast<uint4*>(dst + kpage_chunk_offset_bf16(t, 2 * c + 1, 64)) = hi;
-              } else {
-                const int i = e % D, g = e / D;  // dimension, 16 positions
-                widen16(*reinterpret_cast<const uint4*>(src + fp8_vpage_offset(i, g * 16)), lo, hi);
-                *reinterpret_cast<uint4*>(dst + vpage_chunk_offset_bf16(i, 2 * g)) = lo;
-                *reinterpret_cast<uint4*>(dst + vpage_chunk_offset_bf16(i, 2 * g + 1)) = hi;
-              }
-            }
+            const uint32_t from = smem_u32(src) + from0, to = smem_u32(dst) + to0;
+            if (is_k) widen_page<D, true>(from, to);
+            else widen_page<D, false>(from, to);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -481,7 +484,7 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
     auto bar = [] { asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory"); };
     // waits are voted: tcgen05.ld / st need the whole warp
     auto wait = [&](uint64_t* bar, int bit) {
-      if (ok && !__all_sync(kAll, mbar_wait(bar, phase >> bit & 1))) {
+      if (ok && !__all_sync(kAll, mbar_wait_parked(bar, phase >> bit & 1))) {
         fail(kDevTimeoutMma);
         ok = false;
       }
@@ -489,7 +492,7 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
     for (;; ++pi) {
       const int ps = pi & 1;
       // all softmax warps go on, or none: the barriers wait for every one of them
-      const bool got = ok && __all_sync(kAll, mbar_wait(&piece_full[ps], (pi >> 1) & 1));
+      const bool got = ok && __all_sync(kAll, mbar_wait_parked(&piece_full[ps], (pi >> 1) & 1));
       if (ok && !got) fail(kDevTimeoutFull);
       if (!bar_red_and(1, kSoftmaxThreads, got)) break;
       if (info[ps].pc.head < 0) break;
@@ -510,24 +513,30 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
         const PageSlots sl = slots_s[(k + (two ? u : 2 * u + x)) % kDescs];
         const uint32_t ts = t_s(x, b) + lane_off;
         tc::fence_after_sync();
-        float w[64];
-        tc::tmem_ld32(ts, *reinterpret_cast<float(*)[32]>(w));
-        tc::tmem_ld32(ts + 32, *reinterpret_cast<float(*)[32]>(w + 32));
-        tc::tmem_wait_ld();
-        if (sl.span != kSlotsAll) {
-          const uint64_t vis = sl.span == kSlotsDraft ? anc : tree_page_mask({0, sl.abs_start, sl.span, 0}, hd, pos);
+        // two passes of rolled halves over the scores, which stay in TMEM: unrolled, the roles' loops outgrow the
+        // instruction cache (E4M3 form: @@)
+        float mts = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          float w[32], m8[8];
+          tc::tmem_ld32(ts + 32 * c, w);
+          tc::tmem_wait_ld();
+          if (sl.span != kSlotsAll) {
+            const uint64_t vis = sl.span == kSlotsDraft ? anc : tree_page_mask({0, sl.abs_start, sl.span, 0}, hd, pos);
+            const uint32_t bits = uint32_t(vis >> (32 * c));
 #pragma unroll
-          for (int e = 0; e < 64; ++e)
-            if (!((vis >> e) & 1)) w[e] = -INFINITY;
+            for (int e = 0; e < 32; ++e)
+              if (!((bits >> e) & 1)) w[e] = -INFINITY;
+            tc::tmem_st32(ts + 32 * c, w);
+            tc::tmem_wait_st();
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) m8[i] = fmax3(w[i], w[i + 8], w[i + 16]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) m8[i] = fmaxf(m8[i], w[i + 24]);
+          mts = fmaxf(fmax3(fmax3(m8[0], m8[1], m8[2]), m8[3], m8[4]), fmax3(fmax3(m8[5], m8[6], m8[7]), mts, mts));
         }
-        float m8[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m8[i] = fmaxf(w[i], w[i + 8]);
-#pragma unroll
-        for (int e = 16; e < 64; e += 16)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) m8[i] = fmax3(m8[i], w[e + i], w[e + 8 + i]);
-        const float mts = fmaxf(fmax3(fmax3(m8[0], m8[1], m8[2]), m8[3], m8[4]), fmax3(m8[5], m8[6], m8[7])) * sl2;
+        mts *= sl2;
         // the running reference nearly always holds; where a row of the warp has outgrown it, it moves, and O
         // follows once the previous product is done (the next page's S says so)
         float alpha = 1.f;
@@ -555,24 +564,24 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
         const float base = m == -INFINITY ? 0.f : m;
         const uint64_t nbase2 = f2_pack(-base, -base), scale2 = f2_pack(sl2, sl2);
         uint64_t s2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {  // P of columns 32 c ... goes where those of 16 c ... were
+          float w[32], e0[16], e1[16];  // e0, e1: of pairs of tokens
+          tc::tmem_ld32(ts + 32 * c, w);
+          tc::tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+          for (int e = 0; e < 16; ++e) {
+            float x0, x1;
+            f2_unpack(f2_fma(f2_pack(w[2 * e], w[2 * e + 1]), scale2, nbase2), x0, x1);
+            e0[e] = fast_exp2(x0), e1[e] = fast_exp2(x1);
+            s2[e & 1] = f2_add(s2[e & 1], f2_pack(e0[e], e1[e]));
+          }
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const uint64_t x2 = f2_fma(f2_pack(w[32 * c + 2 * e], w[32 * c + 2 * e + 1]), scale2, nbase2);
-            float e0, e1;
-            if (kPolyMask >> (e % 8) & 1) {
-              exp2_poly_pair(x2, e0, e1);
-            } else {
-              float x0, x1;
-              f2_unpack(x2, x0, x1);
-              e0 = fast_exp2(x0), e1 = fast_exp2(x1);
-            }
-            s2[e & 1] = f2_add(s2[e & 1], f2_pack(e0, e1));
-            // E4M3: the order of the page's positions (pairs 0 4 1 5 2 6 3 7 of every 16 tokens)
-            if constexpr (FP8) pk[(e & 8) | (e & 3) << 1 | (e >> 2 & 1)] = pack_f16x2(e0, e1);
-            else pk[e] = pack_bf16x2(e0, e1);
+            // E4M3: the order of the page's positions (pairs of tokens 0 4 1 5 2 6 3 7 of every 16 tokens)
+            if constexpr (FP8) pk[(e & 8) | (e & 3) << 1 | (e >> 2 & 1)] = pack_f16x2(e0[e], e1[e]);
+            else pk[e] = pack_bf16x2(e0[e], e1[e]);
           }
           tc::tmem_st16(ts + 16 * c, pk);
         }

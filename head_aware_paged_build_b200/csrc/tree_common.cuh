@@ -106,6 +106,14 @@ __device__ __forceinline__ uint64_t tree_visible(uint64_t mask, const HeadDesc& 
   return mask & ~hidden;
 }
 
+// 16 E4M3 codes to two 16-byte chunks of f16, which holds each of them exactly.
+__device__ __forceinline__ void widen16(const uint4& c, uint4& lo, uint4& hi) {
+  lo = make_uint4(e4m3x2_to_f16x2(uint16_t(c.x)), e4m3x2_to_f16x2(uint16_t(c.x >> 16)),
+                  e4m3x2_to_f16x2(uint16_t(c.y)), e4m3x2_to_f16x2(uint16_t(c.y >> 16)));
+  hi = make_uint4(e4m3x2_to_f16x2(uint16_t(c.z)), e4m3x2_to_f16x2(uint16_t(c.z >> 16)),
+                  e4m3x2_to_f16x2(uint16_t(c.w)), e4m3x2_to_f16x2(uint16_t(c.w >> 16)));
+}
+
 // Forms of the draft's page: as an append lays out bf16 and E4M3 pages, and the
 // E4M3 codes widened to f16 in the bf16 pages' layout (V's tokens in the order
 // of the E4M3 pages' positions).
@@ -190,11 +198,10 @@ __device__ __forceinline__ void tree_draft_v(const TreeLaunch& a, const HeadDesc
     for (int y = 0; y < 2; ++y) {
       const uint32_t(&w)[4] = y ? hi : lo;
       if constexpr (FORM == kDraftWide) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          *reinterpret_cast<uint4*>(vdst + vpage_chunk_offset_bf16(i + y, 2 * g + c)) =
-              make_uint4(e4m3x2_to_f16x2(uint16_t(w[2 * c])), e4m3x2_to_f16x2(uint16_t(w[2 * c] >> 16)),
-                         e4m3x2_to_f16x2(uint16_t(w[2 * c + 1])), e4m3x2_to_f16x2(uint16_t(w[2 * c + 1] >> 16)));
+        uint4 o[2];
+        widen16(make_uint4(w[0], w[1], w[2], w[3]), o[0], o[1]);
+        *reinterpret_cast<uint4*>(vdst + vpage_chunk_offset_bf16(i + y, 2 * g)) = o[0];
+        *reinterpret_cast<uint4*>(vdst + vpage_chunk_offset_bf16(i + y, 2 * g + 1)) = o[1];
       } else {
         const int64_t at = FP8 ? fp8_vpage_offset(i + y, g * 16) : vpage_chunk_offset_bf16(i + y, g);
         *reinterpret_cast<uint4*>(vdst + at) = make_uint4(w[0], w[1], w[2], w[3]);
