@@ -65,9 +65,10 @@ struct TreeTc {
   static constexpr int kRaw = 64 * D;        // a page of codes
   static constexpr int kQTiles = WIDE ? 2 : 1;
   // the 224 KB that Q leaves, in pages: K waits for its copy alone, V for a softmax too
-  static constexpr int KS = D == 128 ? (WIDE || FP8 ? 3 : 4) : (FP8 ? 6 : 8);
+  static constexpr int KS = D == 128 ? (WIDE && !FP8 ? 3 : 4) : (FP8 ? 6 : 8);
   static constexpr int VS = D == 128 ? (FP8 ? 4 : WIDE ? 5 : 8) : (FP8 ? 8 : 12);
-  static constexpr int RS = !FP8 ? 0 : D == 128 ? (WIDE ? 3 : 5) : 6;  // pages of codes, K and V each
+  static constexpr int RS = !FP8 ? 0 : D == 128 ? (WIDE ? 2 : 4) : 6;  // pages of codes, K and V each
+  static_assert(!FP8 || (KS % 2 == 0 && VS % 2 == 0 && RS % 2 == 0), "a place of a ring belongs to one widening warp");
   static constexpr int kOffK = kQTiles * kQ;
   static constexpr int kOffV = kOffK + KS * kPage;
   static constexpr int kOffRaw = kOffV + VS * kPage;     // K codes, then V codes
@@ -95,21 +96,31 @@ struct PageSlots {
 constexpr int32_t kSlotsAll = -1;    // every row sees every slot
 constexpr int32_t kSlotsDraft = -2;  // the draft's page
 
-// Half a page of codes to f16, by one warp.  K: a lane is a token, a step 16
-// dimensions; V: a lane is a dimension (of 64), a step 16 positions or the next
-// 64 dimensions.  Both layouts swizzle by XOR, so a step's address is an XOR of
-// the lane's first one.  Four steps at a time in a rolled loop: all unrolled,
-// the roles' loops outgrow the instruction cache (315 us where this takes @@).
+// E4M3 form: parked, so that its sixteen warps poll less (197 us where this takes 165, before the widening below
+// was made cheaper); the bf16 form is 3 % faster without.
+template <bool PARKED>
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity) {
+  return PARKED ? mbar_wait_parked(bar, parity) : mbar_wait(bar, parity);
+}
+
+// A page of codes to f16, by one warp.  K: a lane is a token (then the token 32
+// behind), a step 16 dimensions; V: a lane is a dimension (of 32, then the next
+// 32), a step 16 positions or the dimension 64 behind.  Both layouts swizzle by
+// XOR, so a step's address is an XOR of the lane's first one.  Four steps at a
+// time in a rolled loop: all unrolled, with addresses made afresh, the page took
+// 4300 cycles where this takes 1800.
 template <int D, bool K>
-__device__ __forceinline__ void widen_page(uint32_t from, uint32_t to) {
+__device__ __forceinline__ void widen_page(uint32_t src, uint32_t dst, int lane) {
   constexpr bool kHalves = D == 128 && !K;  // dimensions 64 ... 127 as every other step
 #pragma unroll 1
-  for (int i0 = 0; i0 < D / 16; i0 += 4) {
+  for (int it = 0; it < D / 32; ++it) {
+    const int id = lane + it % 2 * 32, i0 = it / 2 * 4;
+    const uint32_t from = src + (K ? fp8_kpage_offset(id, 0, D) : fp8_vpage_offset(id, 0));
     uint4 c[4], o[2];
 #pragma unroll
     for (int u = 0; u < 4; ++u)
       c[u] = lds128(kHalves ? (from ^ ((i0 / 2 + u / 2) << 4)) + u % 2 * 4096 : from ^ ((i0 + u) << 4));
-    const uint32_t at = K ? to + i0 / 4 * 8192 : to ^ (i0 << 4);
+    const uint32_t to = dst + id * 128 + ((id & 7) << 4), at = K ? to + i0 / 4 * 8192 : to ^ (i0 << 4);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       widen16(c[u], o[0], o[1]);
@@ -164,13 +175,13 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
       mbar_init(&piece_free[x], 8 + 3 + (FP8 ? 4 : 0));  // softmax warps; MMA issuers, V producer; widening warps
     }
     // a page of two query tiles is free when both issuers' products have read it (of one: its stream's, kUses times)
-    for (int s = 0; s < KS; ++s) mbar_init(&k_full[s], FP8 ? 2 : 1), mbar_init(&k_free[s], kUses);
-    for (int s = 0; s < VS; ++s) mbar_init(&v_full[s], FP8 ? 2 : 1), mbar_init(&v_free[s], kUses);
+    for (int s = 0; s < KS; ++s) mbar_init(&k_full[s], 1), mbar_init(&k_free[s], kUses);
+    for (int s = 0; s < VS; ++s) mbar_init(&v_full[s], 1), mbar_init(&v_free[s], kUses);
     if constexpr (FP8) {
       mbar_init(q_ready, 2);
       for (int s = 0; s < RS; ++s) {
-        mbar_init(&kr_full[s], 1), mbar_init(&kr_free[s], 2);
-        mbar_init(&vr_full[s], 1), mbar_init(&vr_free[s], 2);
+        mbar_init(&kr_full[s], 1), mbar_init(&kr_free[s], 1);
+        mbar_init(&vr_full[s], 1), mbar_init(&vr_free[s], 1);
       }
     }
     *abort_flag = 0;
@@ -221,7 +232,7 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
       };
       // a wait by lane 0, its outcome for the warp
       auto wait0 = [&](uint64_t* bar, int parity, int32_t code) {
-        ok = __shfl_sync(kAll, int(lane == 0 && mbar_wait_parked(bar, parity)), 0);
+        ok = __shfl_sync(kAll, int(lane == 0 && tc_wait<FP8>(bar, parity)), 0);
         if (!ok && lane == 0) fail(code);
         return ok;
       };
@@ -282,9 +293,9 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
         }
         // drain: never leave with copies still writing this CTA's shared memory
         if (lane == 0) {
-          if (pi > 0) mbar_wait_parked(q_full, (pi - 1) & 1);
+          if (pi > 0) tc_wait<FP8>(q_full, (pi - 1) & 1);
           for (int j = (k > KR ? k - KR : 0); j < k; ++j)
-            if (!mbar_wait_parked(&kr_full[j % KR], (j / KR) & 1)) break;
+            if (!tc_wait<FP8>(&kr_full[j % KR], (j / KR) & 1)) break;
         }
       } else {
         // ------------------------------ V ------------------------------
@@ -325,7 +336,7 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
         }
         if (lane == 0)
           for (int j = (k > VR ? k - VR : 0); j < k; ++j)
-            if (!mbar_wait_parked(&vr_full[j % VR], (j / VR) & 1)) break;
+            if (!tc_wait<FP8>(&vr_full[j % VR], (j / VR) & 1)) break;
       }
     } else {
       if (lane == 0) {
@@ -336,7 +347,7 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
         const uint32_t q_addr = smem_u32(smem), k_addr = smem_u32(k_ring), v_addr = smem_u32(v_ring);
         uint32_t phase = 0;  // bit b: parity of the phase of the stream's P buffer b
         auto wait = [&](uint64_t* bar, int parity, int32_t code) {
-          ok = mbar_wait_parked(bar, parity);
+          ok = tc_wait<FP8>(bar, parity);
           if (!ok) fail(code);
           return ok;
         };
@@ -400,7 +411,7 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
         }
         // all MMAs issued by this thread complete before TMEM is released
         tc::commit(&done[x]);
-        mbar_wait_parked(&done[x], 0);
+        tc_wait<FP8>(&done[x], 0);
       }
     }
   } else if (FP8 && warp >= 12) {
@@ -408,15 +419,13 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
       // ------------------------------ widening ------------------------------
       tc::reg_dealloc<kRegsMove>();
       const bool is_k = warp < 14;
-      const int half = warp & 1;
+      const int odd = warp & 1;  // the pages it takes: even ones or odd ones
       uint8_t *raw = is_k ? kr_ring : vr_ring, *wide = is_k ? k_ring : v_ring;
       uint64_t *raw_full = is_k ? kr_full : vr_full, *raw_free = is_k ? kr_free : vr_free;
       uint64_t *wide_full = is_k ? k_full : v_full, *wide_free = is_k ? k_free : v_free;
       const int WS = is_k ? KS : VS;
-      const int id = half * 32 + lane;
-      const int from0 = is_k ? fp8_kpage_offset(id, 0, D) : fp8_vpage_offset(id, 0), to0 = id * 128 + ((id & 7) << 4);
       auto wait = [&](uint64_t* bar, int parity) {
-        ok = __all_sync(kAll, mbar_wait_parked(bar, parity));
+        ok = __all_sync(kAll, tc_wait<FP8>(bar, parity));
         if (!ok) fail(kDevTimeoutFull);
         return ok;
       };
@@ -429,7 +438,7 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
           if (!wait(q_full, pi & 1)) break;
           const int bytes = (WIDE && in.pc.nodes > npt ? 2 : 1) * C::kQ;
 #pragma unroll 4
-          for (int e = half * 32 + lane; e < bytes / 16; e += 64) {
+          for (int e = odd * 32 + lane; e < bytes / 16; e += 64) {
             uint4* q = reinterpret_cast<uint4*>(smem) + e;
             const uint4 v = *q;
   *q = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
@@ -440,6 +449,7 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
         }
         const int np = in.pc.p1 - in.pc.p0;
         for (int j = 0; j < np; ++j, ++k) {
+          if ((k & 1) != odd) continue;
           const int rs = k % RS, ws = k % WS;
           if (!wait(&raw_full[rs], (k / RS) & 1)) break;
           if (k >= WS && !wait(&wide_free[ws], ((k / WS) - 1) & 1)) break;
@@ -447,17 +457,14 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
           uint8_t* dst = wide + ws * C::kPage;
           const int kind = is_k ? (slots_s[k % kDescs].span == kSlotsDraft ? kDraftPage : 0) : v_kind[rs];
           if (kind == kDraftPage) {
-            if (half == 0) {
-              if (is_k) tree_draft_k<D, kDraftWide>(a, in.pc.hd, in.pc.n, dst, lane);
-              else tree_draft_v<D, kDraftWide>(a, in.pc.hd, in.pc.n, dst, lane);
-            }
+            if (is_k) tree_draft_k<D, kDraftWide>(a, in.pc.hd, in.pc.n, dst, lane);
+            else tree_draft_v<D, kDraftWide>(a, in.pc.hd, in.pc.n, dst, lane);
           } else if (kind == kNoPage) {  // V: weights of zero meet values of zero
-            for (int e = half * 32 + lane; e < C::kPage / 16; e += 64)
+            for (int e = lane; e < C::kPage / 16; e += 32)
               reinterpret_cast<uint4*>(dst)[e] = make_uint4(0, 0, 0, 0);
           } else {
-            const uint32_t from = smem_u32(src) + from0, to = smem_u32(dst) + to0;
-            if (is_k) widen_page<D, true>(from, to);
-            else widen_page<D, false>(from, to);
+            if (is_k) widen_page<D, true>(smem_u32(src), smem_u32(dst), lane);
+            else widen_page<D, false>(smem_u32(src), smem_u32(dst), lane);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -484,7 +491,7 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
     auto bar = [] { asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory"); };
     // waits are voted: tcgen05.ld / st need the whole warp
     auto wait = [&](uint64_t* bar, int bit) {
-      if (ok && !__all_sync(kAll, mbar_wait_parked(bar, phase >> bit & 1))) {
+      if (ok && !__all_sync(kAll, tc_wait<FP8>(bar, phase >> bit & 1))) {
         fail(kDevTimeoutMma);
         ok = false;
       }
@@ -492,7 +499,7 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
     for (;; ++pi) {
       const int ps = pi & 1;
       // all softmax warps go on, or none: the barriers wait for every one of them
-      const bool got = ok && __all_sync(kAll, mbar_wait_parked(&piece_full[ps], (pi >> 1) & 1));
+      const bool got = ok && __all_sync(kAll, tc_wait<FP8>(&piece_full[ps], (pi >> 1) & 1));
       if (ok && !got) fail(kDevTimeoutFull);
       if (!bar_red_and(1, kSoftmaxThreads, got)) break;
       if (info[ps].pc.head < 0) break;
@@ -516,7 +523,7 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
         // two passes of rolled halves over the scores, which stay in TMEM: unrolled, the roles' loops outgrow the
         // instruction cache (E4M3 form: @@)
         float mts = -INFINITY;
-#pragma unroll 1
+#pragma unroll(FP8 ? 1 : 2)
         for (int c = 0; c < 2; ++c) {
           float w[32], m8[8];
           tc::tmem_ld32(ts + 32 * c, w);
@@ -564,7 +571,7 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
         const float base = m == -INFINITY ? 0.f : m;
         const uint64_t nbase2 = f2_pack(-base, -base), scale2 = f2_pack(sl2, sl2);
         uint64_t s2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-#pragma unroll 1
+#pragma unroll(FP8 ? 1 : 2)
         for (int c = 0; c < 2; ++c) {  // P of columns 32 c ... goes where those of 16 c ... were
           float w[32], e0[16], e1[16];  // e0, e1: of pairs of tokens
           tc::tmem_ld32(ts + 32 * c, w);
