@@ -447,22 +447,40 @@ __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 
 }
 
 // ---------------------------------------------------------------------------
-// fp32 pages: SIMT, FP32 FMA only.  At most 16 rows a group; the draft's rows
-// are read where they are.
+// fp32 pages: SIMT, FP32 FMA only.  At most 16 rows a group.  Pages are copied
+// asynchronously into two stages, rows padded by 16 bytes so that the 128-bit
+// reads of eight lanes (tokens of K, dimensions of V) fall on distinct banks;
+// each K (V) read serves all the rows a thread works for.
 // ---------------------------------------------------------------------------
 constexpr int kF32Threads = 128;
 constexpr int kF32Rows = 16;
 
 template <int D, int P>
+struct TreeF32 {
+  static constexpr int kKPitch = D + 4, kVPitch = P + 4;  // floats
+  static constexpr int kStage = P * kKPitch + D * kVPitch;
+  static constexpr int kBytes = (2 * kStage + kF32Rows * kKPitch + kF32Rows * kVPitch + 3 * kF32Rows) * 4;
+};
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ float dot4(float4 a, float4 b, float s) {
+  return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, s))));
+}
+
+template <int D, int P>
 __global__ void __launch_bounds__(kF32Threads) tree_f32_kernel(TreeLaunch a) {
-  using Split = TreeSplit<1, 4, 8>;
-  constexpr int ACC = kF32Rows * D / kF32Threads;
+  using Split = TreeSplit<1, 4, 2>;
+  using C = TreeF32<D, P>;
+  constexpr int KP = C::kKPitch, VP = C::kVPitch;
+  constexpr int SR = kF32Rows * P / kF32Threads;  // rows a thread scores (of one token)
+  constexpr int OR = kF32Rows * D / kF32Threads;  // rows a thread accumulates (of one dimension)
   extern __shared__ __align__(1024) uint8_t smem[];
-  float* kp = reinterpret_cast<float*>(smem);  // [P][D]
-  float* vp = kp + P * D;                      // [D][P]
-  float* qs = vp + P * D;                      // [rows][D]
-  float* sc = qs + kF32Rows * D;               // [rows][P]
-  float* st = sc + kF32Rows * P;               // alpha, m, l of each row
+  float* stage = reinterpret_cast<float*>(smem);  // 2 x (K [P][KP], V [D][VP])
+  float* qs = stage + 2 * C::kStage;              // [rows][KP]
+  float* sc = qs + kF32Rows * KP;                 // [rows][VP]
+  float* st = sc + kF32Rows * VP;                 // alpha, m, l of each row
   __shared__ int64_t scratch[kF32Threads / 32 + 2];
   __shared__ int pos[kF32Rows];
   __shared__ uint64_t anc[kF32Rows];
@@ -472,93 +490,140 @@ __global__ void __launch_bounds__(kF32Threads) tree_f32_kernel(TreeLaunch a) {
   typename Split::Walk walk = split.walk();
   typename Split::Piece pc;
   while (split.next(a, walk, pc)) {
-    __syncthreads();
     const int rows = pc.nodes * G, rows_max = a.nodes_per_group * G;
     const int64_t q0 = int64_t(pc.hd.b) * a.T + pc.node0;
     auto at_row = [&](int r) { return (q0 + r / G) * a.num_q_heads + pc.hd.kv * G + r % G; };
-    if (tid < 32) {  // one warp holds all rows' nodes
-      uint64_t nodes[2];
-      tree_ancestors(tree_parent(a, pc.hd.b, pc.n, tid), tree_parent(a, pc.hd.b, pc.n, tid + 32), tid, nodes);
-      const uint64_t mask = tree_mask_of(nodes, min(pc.node0 + tid / G, kMaxTreeNodes - 1));
-      if (tid < rows) {
-        anc[tid] = tree_visible(mask, pc.hd);
-        pos[tid] = pc.hd.ctx_len + __popcll(mask) - 1;
-        st[kF32Rows + tid] = -INFINITY, st[2 * kF32Rows + tid] = 0.f;
-      }
-    }
-    for (int e = tid; e < rows * D; e += kF32Threads)
-      qs[e] = static_cast<const float*>(a.q)[at_row(e / D) * D + e % D];
-    float acc[ACC];
-#pragma unroll
-    for (int j = 0; j < ACC; ++j) acc[j] = 0.f;
-    for (int p = pc.p0; p < pc.p1; ++p) {
-      const bool draft = p >= pc.live;
-      const int first = (p - pc.live) * P;  // draft: the page's first node
+    // a page's record (span 0: nothing to see there), and its copy into a stage
+    auto record = [&](int p) {
       PageDesc pg{};
-      if (!draft) {
-        pg = a.pages[pc.hd.vpage_begin + p];
-        if (slot_hi(pg) <= slot_lo(pg)) continue;
-        if (pg.phys < 0 || pg.phys >= a.pool_pages) {
-          if (tid == 0) record_error(a.status, kDevBadPage);
-          continue;
-        }
+      if (p >= pc.live) return pg;
+      pg = a.pages[pc.hd.vpage_begin + p];
+      if (slot_hi(pg) > slot_lo(pg) && (pg.phys < 0 || pg.phys >= a.pool_pages)) {
+        if (tid == 0) record_error(a.status, kDevBadPage);
+        pg.span = 0;
       }
-      __syncthreads();
-      if (!draft) {
-        const uint4* ks = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.kpool) + pg.phys * a.page_bytes);
-        const uint4* vs = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.vpool) + pg.phys * a.page_bytes);
-        for (int e = tid; e < P * D / 4; e += kF32Threads) {
-          reinterpret_cast<uint4*>(kp)[e] = ks[e];
-          reinterpret_cast<uint4*>(vp)[e] = vs[e];
+      return pg;
+    };
+    auto load = [&](int p) {
+      float* kp = stage + (p - pc.p0 & 1) * C::kStage;
+      float* vp = kp + P * KP;
+      if (p < pc.live) {
+        const PageDesc pg = record(p);
+        if (slot_hi(pg) > slot_lo(pg)) {
+          const float* ks = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.kpool) +
+                                                           int64_t(pg.phys) * a.page_bytes);
+          const float* vs = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.vpool) +
+                                                           int64_t(pg.phys) * a.page_bytes);
+          for (int e = tid; e < P * D / 4; e += kF32Threads) {
+            cp_async16(kp + e / (D / 4) * KP + e % (D / 4) * 4, ks + e * 4);
+            cp_async16(vp + e / (P / 4) * VP + e % (P / 4) * 4, vs + e * 4);
+          }
         }
       } else {
+        const int first = (p - pc.live) * P;
         const int64_t base = int64_t(pc.hd.b) * a.ds_seq + int64_t(pc.hd.kv) * a.ds_head;
         for (int e = tid; e < P * D; e += kF32Threads) {
           const int t = e / D, i = e % D;
           const int64_t from = base + (first + t) * a.ds_tok + i;
           const bool in = first + t < pc.n;
-          kp[e] = in ? static_cast<const float*>(a.k_draft)[from] : 0.f;
-          vp[i * P + t] = in ? static_cast<const float*>(a.v_draft)[from] : 0.f;
+          kp[t * KP + i] = in ? static_cast<const float*>(a.k_draft)[from] : 0.f;
+          vp[i * VP + t] = in ? static_cast<const float*>(a.v_draft)[from] : 0.f;
         }
       }
-      __syncthreads();
-      for (int e = tid; e < rows * P; e += kF32Threads) {
-        const int r = e / P, t = e % P;
-        const uint64_t vis = draft ? anc[r] >> first : tree_page_mask(pg, pc.hd, pos[r]);
-        float s = 0.f;
-        for (int i = 0; i < D; ++i) s = fmaf(qs[r * D + i], kp[t * D + i], s);
-        sc[e] = (vis >> t) & 1 ? s * a.scale_log2 : -INFINITY;
-      }
-      __syncthreads();
-      if (tid < rows) {
-        float mx = -INFINITY;
-        for (int t = 0; t < P; ++t) mx = fmaxf(mx, sc[tid * P + t]);
-        const float mo = st[kF32Rows + tid], mn = fmaxf(mo, mx), base = mn == -INFINITY ? 0.f : mn;
-        const float al = exp2f(mo - base);
-        float sum = 0.f;
-        for (int t = 0; t < P; ++t) {
-          const float pv = exp2f(sc[tid * P + t] - base);
-          sc[tid * P + t] = pv;
-          sum += pv;
-        }
-        st[tid] = al;
-        st[kF32Rows + tid] = mn;
-        st[2 * kF32Rows + tid] = st[2 * kF32Rows + tid] * al + sum;
-      }
-      __syncthreads();
-#pragma unroll
-      for (int j = 0; j < ACC; ++j) {
-        const int e = tid + j * kF32Threads, r = e / D, col = e % D;
-        if (r >= rows) continue;
-        float x = acc[j] * st[r];
-        for (int t = 0; t < P; ++t) x = fmaf(sc[r * P + t], vp[col * P + t], x);
-        acc[j] = x;
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    __syncthreads();  // the previous piece's buffers are read
+    load(pc.p0);
+    if (tid < 32) {  // one warp holds all rows' nodes
+      uint64_t nodes[2];
+      tree_ancestors(tree_parent(a, pc.hd.b, pc.n, tid), tree_parent(a, pc.hd.b, pc.n, tid + 32), tid, nodes);
+      const uint64_t mask = tree_mask_of(nodes, min(pc.node0 + tid / G, kMaxTreeNodes - 1));
+      if (tid < kF32Rows) {
+        anc[tid] = tid < rows ? tree_visible(mask, pc.hd) : 0;
+        pos[tid] = pc.hd.ctx_len + __popcll(mask) - 1;
+        st[kF32Rows + tid] = -INFINITY, st[2 * kF32Rows + tid] = 0.f;
       }
     }
-    __syncthreads();
+    for (int e = tid; e < kF32Rows * D / 4; e += kF32Threads) {
+      const int r = e / (D / 4), c = e % (D / 4) * 4;
+      *reinterpret_cast<float4*>(qs + r * KP + c) =
+          r < rows ? *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at_row(r) * D + c)
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float acc[OR];
 #pragma unroll
-    for (int j = 0; j < ACC; ++j) {
-      const int e = tid + j * kF32Threads, r = e / D, col = e % D;
+    for (int j = 0; j < OR; ++j) acc[j] = 0.f;
+    for (int p = pc.p0; p < pc.p1; ++p) {
+      if (p + 1 < pc.p1) load(p + 1);
+      else asm volatile("cp.async.commit_group;" ::: "memory");
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      __syncthreads();
+      const bool draft = p >= pc.live;
+      const int first = (p - pc.live) * P;  // draft: the page's first node
+      const PageDesc pg = record(p);
+      const float* kp = stage + (p - pc.p0 & 1) * C::kStage;
+      const float* vp = kp + P * KP;
+      if (draft || slot_hi(pg) > slot_lo(pg)) {
+        {
+          const int t = tid % P, r0 = tid / P;  // rows r0, r0 + 128 / P, ...
+          float s[SR];
+#pragma unroll
+          for (int j = 0; j < SR; ++j) s[j] = 0.f;
+#pragma unroll 4
+          for (int i = 0; i < D; i += 4) {
+            const float4 kv = *reinterpret_cast<const float4*>(kp + t * KP + i);
+#pragma unroll
+            for (int j = 0; j < SR; ++j)
+              s[j] = dot4(*reinterpret_cast<const float4*>(qs + (r0 + j * (kF32Threads / P)) * KP + i), kv, s[j]);
+          }
+#pragma unroll
+          for (int j = 0; j < SR; ++j) {
+            const int r = r0 + j * (kF32Threads / P);
+            const uint64_t vis = draft ? anc[r] >> first : tree_page_mask(pg, pc.hd, pos[r]);
+            sc[r * VP + t] = (vis >> t) & 1 ? s[j] * a.scale_log2 : -INFINITY;
+          }
+        }
+        __syncthreads();
+        {  // eight threads a row
+          const int r = tid / 8, sub = tid % 8;
+          float x[P / 8], mx = -INFINITY, sum = 0.f;
+#pragma unroll
+          for (int k = 0; k < P / 8; ++k) mx = fmaxf(mx, x[k] = sc[r * VP + sub + 8 * k]);
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          const float mo = st[kF32Rows + r], mn = fmaxf(mo, mx), base = mn == -INFINITY ? 0.f : mn;
+#pragma unroll
+          for (int k = 0; k < P / 8; ++k) {
+            const float e = exp2f(x[k] - base);
+            sc[r * VP + sub + 8 * k] = e;
+            sum += e;
+          }
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          const float al = exp2f(mo - base);
+          __syncwarp();
+          if (sub == 0) st[r] = al, st[kF32Rows + r] = mn, st[2 * kF32Rows + r] = st[2 * kF32Rows + r] * al + sum;
+        }
+        __syncthreads();
+        {
+          const int col = tid % D, r0 = tid / D;  // rows r0, r0 + 128 / D, ...
+#pragma unroll
+          for (int j = 0; j < OR; ++j) acc[j] *= st[r0 + j * (kF32Threads / D)];
+#pragma unroll 4
+          for (int t = 0; t < P; t += 4) {
+            const float4 vv = *reinterpret_cast<const float4*>(vp + col * VP + t);
+#pragma unroll
+            for (int j = 0; j < OR; ++j)
+              acc[j] = dot4(*reinterpret_cast<const float4*>(sc + (r0 + j * (kF32Threads / D)) * VP + t), vv, acc[j]);
+          }
+        }
+      }
+      __syncthreads();  // the stage, the weights and alpha are read
+    }
+    const int col = tid % D, r0 = tid / D;
+#pragma unroll
+    for (int j = 0; j < OR; ++j) {
+      const int r = r0 + j * (kF32Threads / D);
       if (r >= rows) continue;
       const float M = st[kF32Rows + r], L = st[2 * kF32Rows + r];
       if (pc.n_pieces == 1) {
@@ -586,7 +651,7 @@ cudaError_t launch_mma(const TreeLaunch& a, cudaStream_t s) {
 
 template <int D, int P>
 cudaError_t launch_f32(const TreeLaunch& a, cudaStream_t s) {
-  const int bytes = (2 * P * D + kF32Rows * D + kF32Rows * P + 3 * kF32Rows) * 4;
+  constexpr int bytes = TreeF32<D, P>::kBytes;
   auto kern = tree_f32_kernel<D, P>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
