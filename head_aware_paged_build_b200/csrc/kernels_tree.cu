@@ -294,15 +294,38 @@ __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 
                             e4m3x2_to_f16x2(uint16_t(u.y >> 16)));
             }
         } else {
+          // all fragments first (a product waits for its own load, and nothing passes it), and two sums a score,
+          // for chains of half the length
           const int ktok = tok0 + (mi >> 1) * 8 + rr;
+          uint32_t kb[KSTEPS][4];
 #pragma unroll
-          for (int kk = 0; kk < KSTEPS; ++kk) {
-            uint32_t b0, b1, b2, b3;
-            ldmatrix_x4(b0, b1, b2, b3, kst + uint32_t(kpage_chunk_offset_bf16(ktok, 2 * kk + (mi & 1), P)));
-            mma_bf16_16816(sc[0], qa[kk], b0, b1);
-            mma_bf16_16816(sc[1], qa[kk], b2, b3);
+          for (int kk = 0; kk < KSTEPS; ++kk)
+            ldmatrix_x4(kb[kk][0], kb[kk][1], kb[kk][2], kb[kk][3],
+                        kst + uint32_t(kpage_chunk_offset_bf16(ktok, 2 * kk + (mi & 1), P)));
+          float sd[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+          for (int kk = 0; kk < KSTEPS; kk += 2) {
+            mma_bf16_16816(sc[0], qa[kk], kb[kk][0], kb[kk][1]);
+            mma_bf16_16816(sc[1], qa[kk], kb[kk][2], kb[kk][3]);
+            mma_bf16_16816(sd[0], qa[kk + 1], kb[kk + 1][0], kb[kk + 1][1]);
+            mma_bf16_16816(sd[1], qa[kk + 1], kb[kk + 1][2], kb[kk + 1][3]);
           }
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[n][e] += sd[n][e];
         }
+        // V's first fragments come while the weights are made
+        constexpr int VB = 4;
+        uint32_t vb[VB][4];
+        const int vc = (tok0 >> 3) + (mi & 1);
+        auto load_v = [&](int j0) {
+#pragma unroll
+          for (int j = 0; j < VB; ++j)
+            ldmatrix_x4(vb[j][0], vb[j][1], vb[j][2], vb[j][3],
+                        vst + uint32_t(vpage_chunk_offset_bf16((2 * (j0 + j) + (mi >> 1)) * 8 + rr, vc)));
+        };
+        if constexpr (!FP8) load_v(0);
         float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int n = 0; n < 2; ++n)
@@ -352,14 +375,14 @@ __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 
 #pragma unroll
           for (int n = 0; n < 2; ++n)
             pa[2 * n] = pack_bf16x2(pr[n][0], pr[n][1]), pa[2 * n + 1] = pack_bf16x2(pr[n][2], pr[n][3]);
-          const int vc = (tok0 >> 3) + (mi & 1);
 #pragma unroll
-          for (int j = 0; j < NT / 2; ++j) {
-            const int dd = (2 * j + (mi >> 1)) * 8 + rr;
-            uint32_t b0, b1, b2, b3;
-            ldmatrix_x4(b0, b1, b2, b3, vst + uint32_t(vpage_chunk_offset_bf16(dd, vc)));
-            mma_bf16_16816(o[2 * j], pa, b0, b1);
-            mma_bf16_16816(o[2 * j + 1], pa, b2, b3);
+          for (int j0 = 0; j0 < NT / 2; j0 += VB) {
+            if (j0) load_v(j0);
+#pragma unroll
+            for (int j = 0; j < VB; ++j) {
+              mma_bf16_16816(o[2 * (j0 + j)], pa, vb[j][0], vb[j][1]);
+              mma_bf16_16816(o[2 * (j0 + j) + 1], pa, vb[j][2], vb[j][3]);
+            }
           }
         }
       }
