@@ -1,5 +1,5 @@
 // Attention of a drafted tree over the paged cache: the mma.sync kernel
-// (E4M3 pages, and small row counts on bf16 pages) and the fp32 kernel.
+// (up to 32 rows a kv-head) and the fp32 kernel.
 //
 // mma.sync kernel: a producer warp walks the CTA's pieces, hands each to the
 // others a slot ahead (its table entries, parents and Q rows) and streams its
@@ -40,7 +40,7 @@ struct TreeMma {
   static constexpr int kBarOff = kDescOff + kStages * 16;
   static constexpr int kScanOff = kBarOff + (2 * kStages + 6) * 8;
   static constexpr int kInfoOff = kScanOff + ((kThreads / 32 + 2) * 8 + 15) / 16 * 16;
-  using Split = TreeSplit<1, 4, 2>;
+  using Split = TreeSplit<1, 7, 2>;
   using Info = TreePieceInfo<typename Split::Piece>;
   static_assert(kMlOff % 8 == 0 && kQOff % 16 == 0 && kDescOff % 16 == 0 && kBarOff % 8 == 0 && kScanOff % 8 == 0 &&
                     kInfoOff % alignof(Info) == 0,
@@ -684,16 +684,14 @@ cudaError_t launch_f32(const TreeLaunch& a, cudaStream_t s) {
 
 template <int D, bool FP8>
 cudaError_t launch_rows(const TreeLaunch& a, cudaStream_t s) {
-  const int rows = a.nodes_per_group * a.group;
-  if (rows <= 16) return launch_mma<D, FP8, 1, 4>(a, s);
-  return rows <= 32 ? launch_mma<D, FP8, 2, 4>(a, s) : launch_mma<D, FP8, 4, 2>(a, s);
+  return a.nodes_per_group * a.group <= 16 ? launch_mma<D, FP8, 1, 4>(a, s) : launch_mma<D, FP8, 2, 4>(a, s);
 }
 
 }  // namespace
 
-// Rows of a group: 16 or 32 while a sequence's rows fit; more rows of bf16
-// pages go to the tensor cores in tiles of 128, two at a time where a sequence
-// has more; else 64.
+// Rows of a group: 16 or 32 while a sequence's rows fit; more rows of 16-bit and
+// E4M3 pages go to the tensor cores (kernels_tree_tc.cu) in tiles of 128, two at
+// a time where a sequence has more.  fp32 pages: 16.
 TreeConfig tree_config(const sp_plan* plan, int32_t nodes) {
   const int g = plan->group, all = nodes * g;
   TreeConfig c{};
@@ -704,7 +702,7 @@ TreeConfig tree_config(const sp_plan* plan, int32_t nodes) {
     most = (all > 128 ? 2 : 1) * c.nodes_per_tile;
     c.n_ctas = 148;
   } else {
-    const int rows = plan->prob.dtype == SP_F32 || all <= 16 ? 16 : all <= 32 ? 32 : 64;
+    const int rows = plan->prob.dtype == SP_F32 || all <= 16 ? 16 : 32;
     most = rows / g;
     c.n_ctas = rows == 16 ? 2 * 148 : 148;
   }
