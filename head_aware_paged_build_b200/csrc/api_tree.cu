@@ -131,7 +131,7 @@ sp_status segpaged_tree_commit(const sp_plan* plan, void* d_table, const void* k
   CommitLaunch L{};
   L.heads = section<HeadDesc>(d_table, plan->hdr.off_heads);
   L.pages = section<PageDesc>(d_table, plan->hdr.off_pages);
-  L.n_heads = plan->hdr.n_heads;
+  L.n_heads = plan->hdr.n_heads, L.num_kv_heads = plan->prob.num_kv_heads;
   L.D = plan->prob.head_dim, L.P = plan->prob.page_size;
   L.bf16 = plan->prob.dtype == SP_BF16, L.fp8 = plan->fp8;
   L.k_inv = 1.0f / plan->k_scale, L.v_inv = 1.0f / plan->v_scale;

@@ -82,53 +82,51 @@ __device__ __forceinline__ void append_update_eviction(PageDesc* pe, int pos, in
   }
 }
 
+// One 16-byte chunk c of a token's K row, and one value (dimension i) of its V
+// row, into page slot `slot`.  bf16 pages use the swizzled operand layouts, fp32
+// pages row-major K and transposed V, E4M3 pages the codes of the bf16 values
+// times 1 / scale (nearest even, saturating), as the pack writes them.
+template <typename T, int D, int P, bool FP8>
+__device__ __forceinline__ void append_store_k(uint8_t* __restrict__ kdst, int slot, int c, const uint4& v,
+                                               float k_inv) {
+  if constexpr (FP8) {  // 8 values -> 8 codes
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t q[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float x0 = __uint_as_float(w[2 * h] << 16) * k_inv, x1 = __uint_as_float(w[2 * h] & 0xffff0000u) * k_inv;
+      const float x2 = __uint_as_float(w[2 * h + 1] << 16) * k_inv,
+                  x3 = __uint_as_float(w[2 * h + 1] & 0xffff0000u) * k_inv;
+      q[h] = uint32_t(pack_e4m3x2(x0, x1)) | (uint32_t(pack_e4m3x2(x2, x3)) << 16);
+    }
+    *reinterpret_cast<uint2*>(kdst + fp8_kpage_offset(slot, c * 8, D)) = make_uint2(q[0], q[1]);
+  } else if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<uint4*>(kdst + kpage_chunk_offset_bf16(slot, c, P)) = v;
+  } else {
+    *reinterpret_cast<uint4*>(kdst + (int64_t(slot) * D) * 4 + c * 16) = v;
+  }
+}
+template <typename T, int P, bool FP8>
+__device__ __forceinline__ void append_store_v(uint8_t* __restrict__ vdst, int slot, int i, T x, float v_inv) {
+  if constexpr (FP8)
+    vdst[fp8_vpage_offset(i, fp8_vtok_pos(slot))] = uint8_t(pack_e4m3x2(__bfloat162float(x) * v_inv, 0.f));
+  else if constexpr (sizeof(T) == 2)  // transposed V page: row i, token column `slot`
+    *reinterpret_cast<T*>(vdst + vpage_chunk_offset_bf16(i, slot >> 3) + (slot & 7) * 2) = x;
+  else
+    *reinterpret_cast<T*>(vdst + (int64_t(i) * P + slot) * 4) = x;
+}
+
 // Write the new token's K row and V column into page slot `slot` (threads
-// t = first, first + stride, ... of the caller cooperate).  bf16 pages use the
-// swizzled operand layouts, fp32 pages row-major K and transposed V, E4M3
-// pages the codes of the bf16 values times 1 / scale (nearest even,
-// saturating), as the pack writes them.  The new row never overlaps the page,
-// so the loads need not wait for the stores.
+// t = first, first + stride, ... of the caller cooperate).  The new row never
+// overlaps the page, so the loads need not wait for the stores.
 template <typename T, int D, int P, bool FP8>
 __device__ __forceinline__ void append_write_token(const T* __restrict__ kn, const T* __restrict__ vn,
                                                    uint8_t* __restrict__ kdst, uint8_t* __restrict__ vdst, int slot,
                                                    float k_inv, float v_inv, int first, int stride) {
   constexpr int CR = D * int(sizeof(T)) / 16;
-  if constexpr (FP8) {
-    for (int c = first; c < CR; c += stride) {  // 8 values -> 8 codes
-      const uint4 v = reinterpret_cast<const uint4*>(kn)[c];
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      uint32_t q[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float x0 = __uint_as_float(w[2 * h] << 16) * k_inv, x1 = __uint_as_float(w[2 * h] & 0xffff0000u) * k_inv;
-        const float x2 = __uint_as_float(w[2 * h + 1] << 16) * k_inv,
-                    x3 = __uint_as_float(w[2 * h + 1] & 0xffff0000u) * k_inv;
-        q[h] = uint32_t(pack_e4m3x2(x0, x1)) | (uint32_t(pack_e4m3x2(x2, x3)) << 16);
-      }
-      *reinterpret_cast<uint2*>(kdst + fp8_kpage_offset(slot, c * 8, D)) = make_uint2(q[0], q[1]);
-    }
-    for (int i = first; i < D; i += stride) {
-      const float x = __bfloat162float(vn[i]) * v_inv;
-      vdst[fp8_vpage_offset(i, fp8_vtok_pos(slot))] = uint8_t(pack_e4m3x2(x, 0.f));
-    }
-  } else {
-    for (int c = first; c < CR; c += stride) {
-      const uint4 v = reinterpret_cast<const uint4*>(kn)[c];
-      if constexpr (sizeof(T) == 2)
-        *reinterpret_cast<uint4*>(kdst + kpage_chunk_offset_bf16(slot, c, P)) = v;
-      else
-        *reinterpret_cast<uint4*>(kdst + (int64_t(slot) * D) * 4 + c * 16) = v;
-    }
-    for (int i = first; i < D; i += stride) {
-      // transposed V page: row i, token column `slot`
-      int64_t off;
-      if constexpr (sizeof(T) == 2)
-        off = vpage_chunk_offset_bf16(i, slot >> 3) + (slot & 7) * 2;
-      else
-        off = (int64_t(i) * P + slot) * 4;
-      *reinterpret_cast<T*>(vdst + off) = vn[i];
-    }
-  }
+  for (int c = first; c < CR; c += stride)
+    append_store_k<T, D, P, FP8>(kdst, slot, c, reinterpret_cast<const uint4*>(kn)[c], k_inv);
+  for (int i = first; i < D; i += stride) append_store_v<T, P, FP8>(vdst, slot, i, vn[i], v_inv);
 }
 
 }  // namespace sp

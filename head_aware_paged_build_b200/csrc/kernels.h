@@ -210,7 +210,7 @@ cudaError_t launch_tree_join(const TreeLaunch& a, cudaStream_t s);
 struct CommitLaunch {
   HeadDesc* heads;  // device table, updated in place
   PageDesc* pages;
-  int32_t n_heads;
+  int32_t n_heads, num_kv_heads;
   int32_t D, P;
   bool bf16, fp8;
   float k_inv, v_inv;

@@ -520,8 +520,8 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
         const PageSlots sl = slots_s[(k + (two ? u : 2 * u + x)) % kDescs];
         const uint32_t ts = t_s(x, b) + lane_off;
         tc::fence_after_sync();
-        // two passes of rolled halves over the scores, which stay in TMEM: unrolled, the roles' loops outgrow the
-        // instruction cache (E4M3 form: @@)
+        // two passes over the scores, which stay in TMEM.  The E4M3 form rolls the halves: unrolled, the loops of its
+        // roles outgrow the instruction cache (207 us where it took 197); the bf16 form is 3 % faster unrolled
         float mts = -INFINITY;
 #pragma unroll(FP8 ? 1 : 2)
         for (int c = 0; c < 2; ++c) {
