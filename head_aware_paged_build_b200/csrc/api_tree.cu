@@ -179,19 +179,7 @@ sp_status segpaged_reorder(const sp_plan* plan, void* d_table, const int32_t* pa
     if (recs > std::numeric_limits<int32_t>::max()) return fail(SP_ERR_UNSUPPORTED, "more than 2^31 records");
   }
   L.rec_begin[H] = int32_t(recs);
-  // Layout class of a sequence: the first one whose heads have the same kinds, sinks, windows and record counts.
-  auto same = [&](int x, int y) {
-    for (int kv = 0; kv < H; ++kv) {
-      const HeadDesc &p = plan->heads[x * H + kv], &q = plan->heads[y * H + kv];
-      if (p.kind != q.kind || p.sink != q.sink || p.window != q.window || p.n_vpages != q.n_vpages) return false;
-    }
-    return true;
-  };
-  for (int b = 0; b < B; ++b) {
-    int f = 0;
-    while (f < b && !(L.layout[f] == f && same(f, b))) ++f;
-    L.layout[b] = uint16_t(f);
-  }
+  for (int b = 0; b < B; ++b) L.layout[b] = uint16_t(plan->layout[b]);
   const cudaError_t e = launch_reorder(L, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SP_OK : cuda_fail(e, "segpaged_reorder launch");
 }

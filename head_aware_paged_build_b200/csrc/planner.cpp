@@ -8,6 +8,7 @@
 #include <cmath>
 #include <cstring>
 #include <limits>
+#include <map>
 #include <new>
 #include <numeric>
 #include <string>
@@ -555,6 +556,20 @@ sp_status plan_build(sp_plan& pl) {
     }
   }
   pl.n_partial_slots = n_slots;
+
+  // --- layout classes of a ring plan's sequences (segpaged_reorder) ---------------
+  if (ring) {
+    std::map<std::vector<int32_t>, int32_t> first;
+    std::vector<int32_t> key;
+    for (int b = 0; b < p.batch; ++b) {
+      key.clear();
+      for (int kv = 0; kv < p.num_kv_heads; ++kv) {
+        const HeadDesc& h = pl.heads[size_t(b) * p.num_kv_heads + kv];
+        key.insert(key.end(), {h.kind, h.sink, h.window, h.n_vpages});
+      }
+      pl.layout.push_back(first.emplace(key, b).first->second);
+    }
+  }
 
   // --- table blob --------------------------------------------------------------
   TableHeader& H = pl.hdr;

@@ -171,6 +171,8 @@ struct sp_plan {
   bool fp8 = false;                       // pages hold E4M3 codes
   float k_scale = 1.f, v_scale = 1.f;     // E4M3 page scales
   int32_t prefill_tile = 0;
+  std::vector<int32_t> layout;  // ring plans, [batch]: the first sequence whose heads have the same kinds, sinks,
+                                // windows and numbers of page records
   int32_t n_partial_slots = 0;
   int32_t n_counters = 0;      // arrival counters in the workspace (split heads, then merge groups)
   int64_t partial_offset = 0;  // workspace byte offset of the partial slots (status word, then counters)

@@ -272,28 +272,26 @@ struct TreeSplit {
       __syncthreads();
       return v + before;
     };
-    int64_t sum = 0, mine = 0, upto = 0;
-    for (int h0 = 0; h0 < a.n_heads; h0 += NT) {
-      const int h = h0 + int(threadIdx.x);
-      mine = h < a.n_heads ? head_units(a, h) : 0;
-      int64_t total;
-      upto = sum + scan(mine, total);
-      sum += total;
-    }
-    units = sum;
-    ctas = int(min(int64_t(gridDim.x), max(int64_t(1), sum / MIN_UNITS)));
-    if (sum == 0 || int(blockIdx.x) >= ctas) return false;
+    // each thread takes a run of heads: one scan, and the thread whose run holds the CTA's first unit walks it again
+    const int per = (a.n_heads + NT - 1) / NT, h0 = min(a.n_heads, int(threadIdx.x) * per),
+              h1 = min(a.n_heads, h0 + per);
+    int64_t mine = 0;
+#pragma unroll 4
+    for (int h = h0; h < h1; ++h) mine += head_units(a, h);
+    const int64_t upto = scan(mine, units);
+    ctas = int(min(int64_t(gridDim.x), max(int64_t(1), units / MIN_UNITS)));
+    if (units == 0 || int(blockIdx.x) >= ctas) return false;
     const int64_t u0 = cut(blockIdx.x);
-    int64_t run = 0;
-    for (int h0 = 0; h0 < a.n_heads; h0 += NT) {
-      if (a.n_heads > NT) {  // more than one round: sum again, this time to find the head
-        const int h = h0 + int(threadIdx.x);
-        mine = h < a.n_heads ? head_units(a, h) : 0;
-        int64_t total;
-        upto = run + scan(mine, total);
-        run += total;
+    if (u0 < upto && u0 >= upto - mine) {
+      int64_t u = upto - mine;
+      for (int h = h0; h < h1; ++h) {
+        const int64_t w = head_units(a, h);
+        if (u0 < u + w) {
+          scratch[NW] = h, scratch[NW + 1] = u;
+          break;
+        }
+        u += w;
       }
-      if (u0 < upto && u0 >= upto - mine) scratch[NW] = h0 + int(threadIdx.x), scratch[NW + 1] = upto - mine;
     }
     __syncthreads();
     head = int32_t(scratch[NW]);

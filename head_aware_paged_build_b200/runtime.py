@@ -233,7 +233,8 @@ class SegPagedLayer:
         nodes' own keys and values (not in the cache); ``parents``: int32 [B, T], -1 for a root, else an
         earlier node; ``num_nodes``: int32 [B] or None (T each).  Node i at depth d stands at position
         L + d and sees the cache by its head's rule, its ancestors and itself.  Returns (out, lse); rows
-        behind ``num_nodes[b]`` are left as they were (in fresh outputs: zero).  T is at most 64."""
+        behind ``num_nodes[b]`` are left as they were (in fresh outputs: zero).  T is at most 64.  The
+        layer's calls share its workspaces: they must not overlap on the GPU."""
         self._check_tensor(q, "q", self.torch_dtype)
         if q.dim() != 4 or q.shape[0] != self.batch or tuple(q.shape[2:]) != (self.num_q_heads, self.head_dim) or \
                 not q.is_contiguous() or not 1 <= q.shape[1] <= S.SP_TREE_MAX_NODES:

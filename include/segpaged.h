@@ -461,8 +461,9 @@ SP_API sp_status segpaged_decode_step(const sp_plan* plan, void* d_table, const 
  *   parents  device int32 [batch, nodes]: -1 for a root, else below i
  *   num_nodes device int32 [batch] in [0, nodes], or NULL: nodes each
  *   nodes    1 .. 64 (more: SP_ERR_UNSUPPORTED)
- *   out, lse as q, and fp32 [batch, nodes, num_q_heads] or NULL.  Rows at and
- *            behind num_nodes[b] are not read (q, draft, parents) nor written
+ *   out, lse as q, and fp32 [batch, nodes, num_q_heads] or NULL; must not overlap
+ *            the inputs.  Rows at and behind num_nodes[b] have no effect (q,
+ *            draft, parents) and are not written
  *   softmax_scale  <= 0 selects 1/sqrt(head_dim)
  *   workspace device, 256-byte aligned, at least what segpaged_tree_workspace
  *            gives for `nodes` or more.  It begins with a status block of its

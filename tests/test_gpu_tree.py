@@ -152,6 +152,28 @@ def test_more_heads_than_threads():
     Case("bf16", 64, 2, 6, lens, [n % 7 for n in lens], hkv=9).check()
 
 
+@pytest.mark.parametrize("pages,g", [("bf16", 2), ("bf16", 5), ("e4m3", 2), ("e4m3", 5), ("f32", 5)])
+def test_heads_of_a_page_or_two(pages, g):
+    """Hundreds of tiny heads: the split leaves pieces of a single page, where one softmax stream has none."""
+    rng = random.Random(11)
+    for T in (13, 40):
+        lens = [rng.choice([1, 5, 64, 65, 130]) for _ in range(50)]
+        Case(pages, 128, g, T, lens, [rng.randint(0, T) for _ in lens], policy=MIXED[:3], hkv=3).check()
+
+
+def test_layers_on_two_streams_at_once():
+    cases = [Case(pages, 128, 4, 16, (3000, 500), hkv=2, policy=MIXED[:2], seed=i)
+             for i, pages in enumerate(("bf16", "e4m3"))]
+    want = [[x.clone() for x in c.call()] for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[c.call(stream=s) for c, s in zip(cases, streams)] for _ in range(20)]
+    torch.cuda.synchronize()
+    for turn in got:
+        for (o, l), (wo, wl) in zip(turn, want):
+            assert torch.equal(o, wo) and torch.equal(l, wl)
+
+
 def test_sharp_scores_move_the_running_maximum():
     """Scores of a few hundred: the maximum grows from page to page, many weights underflow."""
     c = Case("bf16", 128, 4, 12, (1000, 333), hkv=2, policy=MIXED[:2], scale=2.0)
