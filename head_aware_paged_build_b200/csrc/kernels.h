@@ -3,6 +3,8 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "sp_internal.h"
 
 namespace sp {
@@ -203,6 +205,19 @@ struct TreeConfig {
 };
 TreeConfig tree_config(const sp_plan* plan, int32_t nodes);
 cudaError_t launch_tree(const TreeLaunch& a, const TreeConfig& c, cudaStream_t s);
+// Dynamic shared memory of a kernel, asked for once on each device.
+template <auto KERNEL>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (device & 63);
+  if (device < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && device < 64) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 cudaError_t launch_tree_tc(const TreeLaunch& a, cudaStream_t s);
 cudaError_t launch_tree_join(const TreeLaunch& a, cudaStream_t s);
 

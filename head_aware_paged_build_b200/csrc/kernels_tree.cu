@@ -24,7 +24,8 @@ constexpr float kLazyLog2 = 8.f;
 template <int D, bool FP8, int WR, int WT>
 struct TreeMma {
   static constexpr int kConsumers = WR * WT;
-  // 16-row form: two CTAs an SM, whose 12 warps may have 168 registers a thread; a 14th would cost 40 of them
+  // 16-row form: two CTAs an SM, whose 12 warps may have 168 registers a thread; a 14th would cost 40 of them, so
+  // the producer writes the draft's K
   static constexpr int kDraftWarps = WR > 1 ? 2 : 1;
   static constexpr int kThreads = (kConsumers + 1 + kDraftWarps) * 32;
   static constexpr int kRows = 16 * WR;
@@ -56,6 +57,7 @@ __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 
   constexpr int P = 64, PB = C::kPageBytes, NST = C::kStages, NC = C::kConsumers, ND = C::kDraftWarps;
   constexpr int KSTEPS = D / 16, NT = D / 8, CHUNKS = 4 / WT;
   constexpr uint32_t kAll = 0xffffffffu;
+  constexpr DraftForm FORM = FP8 ? kDraftE4m3 : kDraftBf16;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* stage = smem;
   float* mbuf = reinterpret_cast<float*>(smem + C::kMergeOff);
@@ -136,9 +138,14 @@ __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 
         if (p >= pc.live) {  // the draft's page: its writers arrive when they have filled it
           if (lane == 0) {
             sdesc[s] = PageDesc{kDraftPage, 0, 0, pc.head};
-            mbar_arrive(&full[s]);
             mbar_arrive(&draft_go[ps]);  // the stage is free
           }
+          if constexpr (ND == 1) {
+            tree_draft_k<D, FORM>(a, pc.hd, pc.n, kd, lane);
+            fence_proxy_async_smem();  // before a later bulk copy into this stage
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[s]);
           continue;
         }
         if (lane == 0) {
@@ -180,8 +187,7 @@ __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 
 
   if (warp > NC) {
     // ------------------------------ draft page ------------------------------
-    constexpr DraftForm FORM = FP8 ? kDraftE4m3 : kDraftBf16;
-    const bool does_k = warp == NC + 1, does_v = warp == NC + ND;
+    const bool does_k = ND == 2 && warp == NC + 1, does_v = warp == NC + ND;
     for (int pi = 0;; ++pi) {
       const int ps = pi & 1;
       if (!__all_sync(kAll, mbar_wait(&piece_full[ps], (pi >> 1) & 1))) break;
@@ -665,20 +671,18 @@ __global__ void __launch_bounds__(kF32Threads) tree_f32_kernel(TreeLaunch a) {
 template <int D, bool FP8, int WR, int WT>
 cudaError_t launch_mma(const TreeLaunch& a, cudaStream_t s) {
   using C = TreeMma<D, FP8, WR, WT>;
-  auto kern = tree_mma_kernel<D, FP8, WR, WT>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
+  const cudaError_t e = allow_smem<tree_mma_kernel<D, FP8, WR, WT>>(C::kBytes);
   if (e != cudaSuccess) return e;
-  kern<<<a.n_ctas, C::kThreads, C::kBytes, s>>>(a);
+  tree_mma_kernel<D, FP8, WR, WT><<<a.n_ctas, C::kThreads, C::kBytes, s>>>(a);
   return cudaGetLastError();
 }
 
 template <int D, int P>
 cudaError_t launch_f32(const TreeLaunch& a, cudaStream_t s) {
   constexpr int bytes = TreeF32<D, P>::kBytes;
-  auto kern = tree_f32_kernel<D, P>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  const cudaError_t e = allow_smem<tree_f32_kernel<D, P>>(bytes);
   if (e != cudaSuccess) return e;
-  kern<<<a.n_ctas, kF32Threads, bytes, s>>>(a);
+  tree_f32_kernel<D, P><<<a.n_ctas, kF32Threads, bytes, s>>>(a);
   return cudaGetLastError();
 }
 

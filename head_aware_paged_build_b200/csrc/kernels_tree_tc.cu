@@ -706,10 +706,9 @@ cudaError_t launch(const TreeLaunch& a, int64_t total_rows, cudaStream_t s) {
   CUtensorMap qmap;
   cudaError_t e = encode_query_map(&qmap, a.q, D, a.num_q_heads, total_rows, a.group, a.nodes_per_tile);
   if (e != cudaSuccess) return e;
-  auto kern = tree_tc_kernel<D, WIDE, FP8>;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
+  e = allow_smem<tree_tc_kernel<D, WIDE, FP8>>(C::kBytes);
   if (e != cudaSuccess) return e;
-  kern<<<a.n_ctas, C::kThreads, C::kBytes, s>>>(qmap, a);
+  tree_tc_kernel<D, WIDE, FP8><<<a.n_ctas, C::kThreads, C::kBytes, s>>>(qmap, a);
   return cudaGetLastError();
 }
 

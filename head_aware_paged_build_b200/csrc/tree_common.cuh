@@ -243,8 +243,15 @@ struct TreeSplit {
     if (bad && blockIdx.x == 0) record_error(a.status, kDevBadTree);
     return w.per * w.groups;
   }
-  __device__ __forceinline__ int64_t cut(int64_t c) const { return c * units / ctas; }
-  __device__ __forceinline__ int cta_of(int64_t u) const { return int(((u + 1) * ctas + units - 1) / units) - 1; }
+  // (32-bit divisions where the line is short enough: a small call makes a dozen of them one after another)
+  __device__ __forceinline__ bool small() const { return units < (1 << 22); }  // units x CTAs, and units more: < 2^32
+  __device__ __forceinline__ int64_t cut(int64_t c) const {
+    return small() ? int64_t(uint32_t(c) * uint32_t(units) / uint32_t(ctas)) : c * units / ctas;
+  }
+  __device__ __forceinline__ int cta_of(int64_t u) const {
+    if (small()) return int((uint32_t(u + 1) * uint32_t(ctas) + uint32_t(units) - 1) / uint32_t(units)) - 1;
+    return int(((u + 1) * ctas + units - 1) / units) - 1;
+  }
 
   // All NT threads of the block.  scratch: NT / 32 + 2 int64 in shared memory.
   // Returns false when this CTA has no work.  Also lets the joining kernel's blocks be placed.

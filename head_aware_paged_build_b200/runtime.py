@@ -215,13 +215,14 @@ class SegPagedLayer:
         self._check_tensor(k, "k_draft", self.torch_dtype)
         self._check_tensor(v, "v_draft", self.torch_dtype)
         want = (self.batch, nodes, self.num_kv_heads, self.head_dim)
-        if tuple(k.shape) != want or k.shape != v.shape or k.stride() != v.stride() or k.stride(-1) != 1:
+        strides = k.stride()
+        if k.shape != want or v.shape != want or strides != v.stride() or strides[-1] != 1:
             raise ValueError(f"k_draft / v_draft must be {want} with the same strides, head_dim contiguous; got "
                              f"{tuple(k.shape)} and {tuple(v.shape)}")
 
     def _check_index(self, t: torch.Tensor, what: str, *shape: int) -> None:
         self._check_tensor(t, what, torch.int32)
-        if tuple(t.shape) != shape or not t.is_contiguous():
+        if t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{what} must be contiguous {shape}, got {tuple(t.shape)}")
 
     def tree_attention(self, q: torch.Tensor, k_draft: torch.Tensor, v_draft: torch.Tensor, parents: torch.Tensor,
@@ -236,12 +237,12 @@ class SegPagedLayer:
         behind ``num_nodes[b]`` are left as they were (in fresh outputs: zero).  T is at most 64.  The
         layer's calls share its workspaces: they must not overlap on the GPU."""
         self._check_tensor(q, "q", self.torch_dtype)
-        if q.dim() != 4 or q.shape[0] != self.batch or tuple(q.shape[2:]) != (self.num_q_heads, self.head_dim) or \
-                not q.is_contiguous() or not 1 <= q.shape[1] <= S.SP_TREE_MAX_NODES:
+        T = q.shape[1] if q.dim() == 4 else 0
+        if not 1 <= T <= S.SP_TREE_MAX_NODES or not q.is_contiguous() or \
+                q.shape != (self.batch, T, self.num_q_heads, self.head_dim):
             raise ValueError(f"q must be contiguous [{self.batch}, 1 .. {S.SP_TREE_MAX_NODES}, {self.num_q_heads}, "
                              f"{self.head_dim}], got {tuple(q.shape)}")
-        T = q.shape[1]
-        rows = tuple(q.shape[:3])
+        rows = (self.batch, T, self.num_q_heads)
         self._check_draft(k_draft, v_draft, T)
         self._check_index(parents, "parents", self.batch, T)
         if num_nodes is not None:
@@ -252,7 +253,7 @@ class SegPagedLayer:
                 raise ValueError(f"out must be contiguous {tuple(q.shape)}, got {tuple(out.shape)}")
         if lse is not None:
             self._check_tensor(lse, "lse", torch.float32)
-            if tuple(lse.shape) != rows or not lse.is_contiguous():
+            if lse.shape != rows or not lse.is_contiguous():
                 raise ValueError(f"lse must be contiguous {rows}, got {tuple(lse.shape)}")
         if self._elsewhere(stream):  # fresh outputs and workspaces belong to the call's stream
             with _on(self.k_pool.device, stream):
