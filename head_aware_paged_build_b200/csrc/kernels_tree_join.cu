@@ -34,27 +34,37 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeLaunch a) {
   constexpr int R1 = kJoinThreads / CG;   // rows of an item in one part
   constexpr int PER = kTreeMaxCtas / 32;
   __shared__ int s_end[kTreeMaxCtas];  // items up to and with each CTA's group
+  __shared__ TreeJoin s_join[kTreeMaxCtas];
   __shared__ float s_part[kJoinThreads][kCols + 1];
-  __shared__ float2 s_ml[kJoinThreads];
+  __shared__ float s_m[kJoinThreads], s_l[kJoinThreads];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31;
-  for (int c = tid; c < a.n_ctas; c += kJoinThreads) {
-    const int n = a.joins[c].n_pieces, per = R1 / join_parts(n);
-    s_end[c] = n > 0 ? (a.joins[c].rows + per - 1) / per : 0;
+  for (int c = tid; c < kTreeMaxCtas; c += kJoinThreads) {
+    int4 head = make_int4(0, 0, 0, 0), rest = head;  // n_pieces, first_slot, rows, b; the others
+    if (c < a.n_ctas) {
+      head = __ldcg(reinterpret_cast<const int4*>(a.joins + c));
+      rest = __ldcg(reinterpret_cast<const int4*>(a.joins + c) + 1);
+    }
+    const int per = R1 / join_parts(head.x);
+    s_end[c] = head.x > 0 ? (head.z + per - 1) / per : 0;
+    reinterpret_cast<int4*>(s_join + c)[0] = head;
+    reinterpret_cast<int4*>(s_join + c)[1] = rest;
   }
   __syncthreads();
-  if (tid < 32) {
-    int items = 0;
-    for (int i = 0; i < PER; ++i)
-      if (lane * PER + i < a.n_ctas) s_end[lane * PER + i] = items += s_end[lane * PER + i];
-    int upto = items;
+  if (tid < 32) {  // a lane takes a run of CTAs
+    int items[PER], sum = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) items[i] = s_end[lane * PER + i];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) items[i] = sum += items[i];
+    int upto = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += x;
     }
-    for (int i = 0; i < PER; ++i)
-      if (lane * PER + i < a.n_ctas) s_end[lane * PER + i] += upto - items;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) s_end[lane * PER + i] = items[i] + upto - sum;
   }
   __syncthreads();
   const int rows_max = a.nodes_per_group * a.group;
@@ -67,7 +77,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeLaunch a) {
       if (s_end[mid] > item) hi = mid;
       else lo = mid + 1;
     }
-    const TreeJoin jn = a.joins[lo];
+    const TreeJoin& jn = s_join[lo];
     const int parts = join_parts(jn.n_pieces), R = R1 / parts;
     const int row0 = (item - (lo ? s_end[lo - 1] : 0)) * R;
     // thread = (part, column group, row of the item)
@@ -134,30 +144,33 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeLaunch a) {
       if (cg == 0 && a.lse) a.lse[at] = (m + log2f(l)) * kTreeLn2;
       continue;
     }
-    // the parts meet, in order: a thread takes single columns
-    __syncthreads();  // the previous item's sums are read
+    // the parts meet: each brings its sums to the common maximum, then a thread adds up single columns in order
+    s_m[tid] = m;
+    __syncthreads();  // (also: the previous item's sums are read)
+    float M = -INFINITY;
+    for (int p = 0; p < parts; ++p) M = fmaxf(M, s_m[p * R * CG + cg * R + tid % R]);
+    const float f = exp2f(m - (M == -INFINITY ? 0.f : M));
 #pragma unroll
-    for (int e = 0; e < kCols; ++e) s_part[tid][e] = acc[e];
-    s_ml[tid] = make_float2(m, l);
+    for (int e = 0; e < kCols; ++e) s_part[tid][e] = acc[e] * f;
+    s_l[tid] = l * f;
     __syncthreads();
     for (int e = tid; e < R * D; e += kJoinThreads) {
       const int r = e / D, col = e % D, at0 = col / kCols * R + r;  // the thread of part 0
-      if (row0 + r >= jn.rows) continue;
-      float M = -INFINITY;
-      for (int p = 0; p < parts; ++p) M = fmaxf(M, s_ml[p * R * CG + at0].x);
-      const float base = M == -INFINITY ? 0.f : M;
       float L = 0.f, x = 0.f;
       for (int p = 0; p < parts; ++p) {
-        const float2 ml = s_ml[p * R * CG + at0];
-        const float f = exp2f(ml.x - base);
-        L += f * ml.y;
-        x += f * s_part[p * R * CG + at0][col % kCols];
+        L += s_l[p * R * CG + at0];
+        x += s_part[p * R * CG + at0][col % kCols];
       }
+      if (row0 + r >= jn.rows) continue;
       const int64_t at = out_row(row0 + r);
       x *= a.v_scale / L;
       if constexpr (sizeof(T) == 2) static_cast<__nv_bfloat16*>(a.out)[at * D + col] = __float2bfloat16_rn(x);
       else static_cast<float*>(a.out)[at * D + col] = x;
-      if (col == 0 && a.lse) a.lse[at] = (M + log2f(L)) * kTreeLn2;
+    }
+    if (part == 0 && cg == 0 && row < jn.rows && a.lse) {
+      float L = 0.f;
+      for (int p = 0; p < parts; ++p) L += s_l[p * R * CG + tid % R];
+      a.lse[out_row(row)] = (M + log2f(L)) * kTreeLn2;
     }
   }
 }
