@@ -4,15 +4,20 @@
 // One persistent CTA an SM walks its pieces of the work line (tree_common.cuh).
 // A query tile is up to 128 rows (nodes x the group's q-heads, TMEM lane = row),
 // a KV tile one page, 64 tokens.  Two softmax streams share the tensor core:
-//   a piece of one query tile   stream x takes pages x, x + 2, ... with its own
-//                               running maximum, sum and O; the streams' results
-//                               join at the end of the piece;
-//   a piece of two query tiles  (WIDE) stream x takes query tile x over every
-//                               page, so one staged page feeds 256 rows.
+//   one query tile a piece       stream x takes the pages of parity x with its own
+//                                running maximum, sum and O; the streams' results
+//                                join at the end of the piece;
+//   two query tiles (WIDE)       stream x takes query tile x over every page, so one
+//                                staged page feeds 256 rows (a piece with rows for one
+//                                tile leaves stream 1 idle).
+// A barrier's phase is waited for by parity, so a waiter must not be a phase ahead
+// or behind: every role waits for every phase of a barrier it uses, or for all of
+// the barriers it owns.  Hence pages alternate by their number in the CTA, not in
+// the piece, over rings of even length: a place of a ring belongs to one stream.
 // A stream has two S buffers of 64 columns: while its softmax works on one page's
 // scores, the tensor core makes the next page's S and the last one's O += P V.
 // (With one buffer of 128 tokens a stream, a softmax waited for its own two
-// products: 251 us where this form takes 222 on 64 nodes of the 32K layer.)
+// products: 251 us where this form takes 221 on 64 nodes of the 32K layer.)
 // One query tile reads its K/V once and is bound by HBM; two tiles a CTA double
 // the products on the same bytes and are bound by the softmax's arithmetic.
 //
@@ -79,6 +84,7 @@ struct TreeTc {
   using Info = TreePieceInfo<typename Split::Piece>;
   static constexpr int kOffBar = kOffInfo + (2 * int(sizeof(Info)) + 7) / 8 * 8;
   static constexpr int kBytes = kOffBar + (22 + 2 * KS + 2 * VS + 4 * RS) * 8 + 8 + 8 * (RS > 0);
+  static_assert(WIDE || (KS % 2 == 0 && VS % 2 == 0), "a place of a ring belongs to one stream");
   static_assert(KS + RS + 4 <= kDescs, "page descriptions");
   static_assert(kBytes <= 232448, "shared memory of a CTA");
   static_assert(kOffK % 1024 == 0 && kPage % 1024 == 0 && kRaw % 1024 == 0 && kOffMl % 8 == 0 && kOffDesc % 8 == 0 &&
@@ -174,7 +180,7 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
       mbar_init(&piece_full[x], 1);
       mbar_init(&piece_free[x], 8 + 3 + (FP8 ? 4 : 0));  // softmax warps; MMA issuers, V producer; widening warps
     }
-    // a page of two query tiles is free when both issuers' products have read it (of one: its stream's, kUses times)
+    // a page of two query tiles is free when both issuers' products have read it
     for (int s = 0; s < KS; ++s) mbar_init(&k_full[s], 1), mbar_init(&k_free[s], kUses);
     for (int s = 0; s < VS; ++s) mbar_init(&v_full[s], 1), mbar_init(&v_free[s], kUses);
     if constexpr (FP8) {
@@ -243,7 +249,7 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
         typename Split::Piece pc;
         auto slot_free = [&] { return pi < 2 || wait0(&piece_free[pi & 1], ((pi >> 1) - 1) & 1, kDevTimeoutEmpty); };
         while (ok && split.next(a, walk, pc)) {
-          const bool two = WIDE && pc.nodes > npt;
+          const int tiles = WIDE && pc.nodes > npt ? 2 : 1;
           fetch(pc, pc.p0);
           if (!slot_free()) break;
           tree_publish(a, pc, k, lane, info[pi & 1]);
@@ -275,8 +281,8 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
             if (p == pc.p0) {  // behind the first K page: Q's place is free only after the previous piece's last S
               if (pi > 0 && !wait0(q_free, (pi - 1) & 1, kDevTimeoutMma)) break;
               if (lane == 0) {
-                mbar_arrive_expect_tx(q_full, (two ? 2 : 1) * (D / 64) * npt * G * 128);
-                for (int x = 0; x < (two ? 2 : 1); ++x)
+                mbar_arrive_expect_tx(q_full, tiles * (D / 64) * npt * G * 128);
+                for (int x = 0; x < tiles; ++x)
 #pragma unroll
                   for (int h = 0; h < D / 64; ++h)
                     tc::tma_load_3d(smem + x * C::kQ + h * 16384, &qmap, h * 64, pc.hd.kv * G,
@@ -351,19 +357,15 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
           if (!ok) fail(code);
           return ok;
         };
-        // the stream's last product of a page is issued: its place is free when that has run
-        auto free_page = [&](uint64_t* bar, bool two) {
-          tc::commit(bar);
-          if (WIDE && !two) tc::commit(bar);
-        };
         while (ok) {
           const int ps = pi & 1;
           if (!wait(&piece_full[ps], (pi >> 1) & 1, kDevTimeoutFull) || info[ps].pc.head < 0) break;
-          const bool two = WIDE && info[ps].pc.nodes > npt;
-          const int np = info[ps].pc.p1 - info[ps].pc.p0, U = two ? np : (np + 1 - x) / 2;
+          const int np = info[ps].pc.p1 - info[ps].pc.p0, j0 = (x - k) & 1;
+          const bool lone = WIDE && info[ps].pc.nodes <= npt;  // rows for one tile
+          const int U = !WIDE ? (np + 1 - j0) / 2 : lone && x == 1 ? 0 : np;
           mbar_arrive(&piece_free[ps]);
-          auto page_of = [&](int u) { return k + (two ? u : 2 * u + x); };
-          const uint64_t qd = tc::smem_desc_sw128(q_addr + (two ? x : 0) * C::kQ);
+          auto page_of = [&](int u) { return k + (WIDE ? u : 2 * u + j0); };
+          const uint64_t qd = tc::smem_desc_sw128(q_addr + (WIDE ? x : 0) * C::kQ);
           auto wait_k = [&](int u) {
             const int pg = page_of(u);
             return wait(&k_full[pg % KS], (pg / KS) & 1, kDevTimeoutFull);
@@ -376,13 +378,19 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
               tc::mma_f16_ss(t_s(x, u & 1), qd + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
                               kd + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
             tc::commit(&s_full[2 * x + (u & 1)]);
-            free_page(&k_free[pg % KS], two);
+            tc::commit(&k_free[pg % KS]);
             if (u == U - 1) tc::commit(q_free);
           };
-          // (waited for even without a page: a wait left out would leave the next one a phase ahead)
           if (!wait(FP8 ? q_ready : q_full, pi & 1, kDevTimeoutFull)) break;
-          if (U == 0) {  // a piece of one page
+          if (U == 0) {
             mbar_arrive(q_free);
+            for (int j = 0; WIDE && j < np; ++j) {  // the pages pass it by
+              const int pg = k + j;
+              if (!wait(&k_full[pg % KS], (pg / KS) & 1, kDevTimeoutFull)) break;
+              mbar_arrive(&k_free[pg % KS]);
+              if (!wait(&v_full[pg % VS], (pg / VS) & 1, kDevTimeoutFull)) break;
+              mbar_arrive(&v_free[pg % VS]);
+            }
           } else {
             for (int u = 0; u < min(2, U) && wait_k(u); ++u) {
               tc::fence_after_sync();
@@ -403,7 +411,7 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
               // the next S also says that this product is done; the last two have no next S
               if (u + 2 < U) issue_s(u + 2);
               else tc::commit(u + 1 < U ? &pv_done[x] : &o_done[x]);
-              free_page(&v_free[pg % VS], two);
+              tc::commit(&v_free[pg % VS]);
             }
           }
           if (*abort_flag) break;
@@ -441,7 +449,7 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
           for (int e = odd * 32 + lane; e < bytes / 16; e += 64) {
             uint4* q = reinterpret_cast<uint4*>(smem) + e;
             const uint4 v = *q;
-  *q = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
+            *q = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -505,10 +513,10 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
       if (info[ps].pc.head < 0) break;
       const typename Split::Piece& pc = info[ps].pc;
       const HeadDesc hd = pc.hd;
-      const bool two = WIDE && pc.nodes > npt;
-      const int np = pc.p1 - pc.p0, U = two ? np : (np + 1 - x) / 2;
-      const int first_node = pc.node0 + (two ? x * npt : 0);
+      const int first_node = pc.node0 + (WIDE ? x * npt : 0);
       const int rows = min(npt, pc.node0 + pc.nodes - first_node) * G;
+      const int np = pc.p1 - pc.p0, j0 = (x - k) & 1;
+      const int U = !WIDE ? (np + 1 - j0) / 2 : rows > 0 ? np : 0;
       const bool busy = quarter * 32 < rows;  // any row in this warp
       uint64_t nodes[2];
       tree_ancestors(info[ps].up[lane], info[ps].up[lane + 32], lane, nodes);
@@ -517,7 +525,7 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
       const int pos = hd.ctx_len + __popcll(mask) - 1;
       float m = -INFINITY, l = 0.f;
       auto page_scores = [&](int u, int b) {
-        const PageSlots sl = slots_s[(k + (two ? u : 2 * u + x)) % kDescs];
+        const PageSlots sl = slots_s[(k + (WIDE ? u : 2 * u + j0)) % kDescs];
         const uint32_t ts = t_s(x, b) + lane_off;
         tc::fence_after_sync();
         // two passes over the scores, which stay in TMEM.  The E4M3 form rolls the halves: unrolled, the loops of its
@@ -613,7 +621,7 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
         phase ^= 1u << 3;
       }
       tc::fence_after_sync();
-      const int row_in_group = two ? x * npt * G + r : r;
+      const int row_in_group = WIDE ? x * npt * G + r : r;
       const bool valid = r < rows;
       const bool whole = pc.n_pieces == 1;
       float* slot = a.partial + int64_t(pc.slot) * tree_slot_floats(a);
@@ -642,7 +650,7 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
         if (!whole) *reinterpret_cast<float2*>(slot + rows_max * D + 2 * row_in_group) = make_float2(mm, ll);
         else if (a.lse) a.lse[at] = (mm + log2f(ll)) * kTreeLn2;
       };
-      if (two) {
+      if constexpr (WIDE) {
         if (ok && busy) {
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
@@ -667,17 +675,15 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
 #pragma unroll
           for (int c = 0; c < D / 64; ++c) {
             const int col = x * (D / 2) + 32 * c;
-            float o[32];
-            tc::tmem_ld32(t_o(0) + lane_off + col, o);
-            tc::tmem_wait_ld();
+            float o[32] = {};
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= f0;
-            if (np > 1) {  // stream 1 had a page
-              float o1[32];
-              tc::tmem_ld32(t_o(1) + lane_off + col, o1);
+            for (int y = 0; y < 2; ++y) {
+              if ((np + 1 - ((y - k) & 1)) / 2 == 0) continue;  // stream y had no page
+              float v[32];
+              tc::tmem_ld32(t_o(y) + lane_off + col, v);
               tc::tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] += f1 * o1[e];
+              for (int e = 0; e < 32; ++e) o[e] += (y ? f1 : f0) * v[e];
             }
             put(o, col, a.v_scale / L);
           }

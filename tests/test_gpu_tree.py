@@ -147,6 +147,24 @@ def test_a_long_context_is_split_over_many_ctas(pages, T, g):
     Case(pages, 128, g, T, (70001, 1, 3000), hkv=2, policy=[("global", 0, 0), ("local", 4, 8000)]).check()
 
 
+@pytest.mark.parametrize("pages,d,T,g", [("bf16", 128, 40, 8), ("bf16", 64, 40, 8), ("e4m3", 128, 40, 8),
+                                         ("e4m3", 64, 40, 8), ("bf16", 128, 13, 8), ("e4m3", 128, 13, 8)])
+def test_pieces_of_one_and_two_tiles_repeat_bit_for_bit(pages, d, T, g):
+    """A CTA's pieces alternate between one and two query tiles and between odd and even numbers of pages: a
+    barrier that a role passes a phase early shows as another call's bits."""
+    lens = [40001, 1, 700, 129, 9000, 64, 20011, 333]
+    counts = [T, T, 1, T, T // 2, T, T - 3, 5]
+    case = Case(pages, d, g, T, lens, counts, hkv=3, policy=[("global", 0, 0), ("local", 4, 3000), ("local", 1, 70)])
+    case.check()
+    first = None
+    for turn in range(200):
+        now = torch.zeros_like(case.q), torch.zeros(case.q.shape[:3], device="cuda")
+        case.call(out=now[0], lse=now[1])
+        first = first or now
+        assert all(torch.equal(x, y) for x, y in zip(now, first)), turn
+    assert case.layer.device_status() == 0
+
+
 def test_more_heads_than_threads():
     lens = [random.Random(5).randint(1, 200) for _ in range(70)]
     Case("bf16", 64, 2, 6, lens, [n % 7 for n in lens], hkv=9).check()
