@@ -22,9 +22,11 @@ T* section(const void* d_table, int64_t off) {
   return reinterpret_cast<T*>(const_cast<uint8_t*>(static_cast<const uint8_t*>(d_table)) + off);
 }
 
-// Workspace: status block | descriptions of split row groups, one a CTA | two
-// partial slots a CTA.
-constexpr int64_t kTreePartialOffset = kStatusBytes + (kTreeMaxCtas * int64_t(sizeof(TreeJoin)) + 255) / 256 * 256;
+// Workspace: status block | descriptions of split row groups, one a CTA |
+// tickets (the same place whatever the tree's size, so that calls of different
+// sizes leave each other's at zero) | two partial slots a CTA.
+constexpr int64_t kTreeTicketOffset = kStatusBytes + (kTreeMaxCtas * int64_t(sizeof(TreeJoin)) + 255) / 256 * 256;
+constexpr int64_t kTreePartialOffset = kTreeTicketOffset + kTreeHeadsHere * kMaxTreeNodes * 4;
 
 int64_t tree_workspace_bytes(const sp_plan* plan, int32_t nodes) {
   const TreeConfig c = tree_config(plan, nodes);
@@ -104,9 +106,10 @@ sp_status segpaged_tree_attention(const sp_plan* plan, const void* d_table, cons
   L.nodes_per_group = c.nodes_per_group, L.nodes_per_tile = c.nodes_per_tile, L.n_ctas = c.n_ctas;
   L.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kTreePartialOffset);
   L.joins = reinterpret_cast<TreeJoin*>(static_cast<uint8_t*>(workspace) + kStatusBytes);
+  if (c.joins_here) L.tickets = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + kTreeTicketOffset);
   L.status = static_cast<int32_t*>(workspace);
   cudaError_t e = launch_tree(L, c, static_cast<cudaStream_t>(stream));
-  if (e == cudaSuccess) e = launch_tree_join(L, static_cast<cudaStream_t>(stream));
+  if (e == cudaSuccess && !c.joins_here) e = launch_tree_join(L, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SP_OK : cuda_fail(e, "segpaged_tree_attention launch");
 }
 

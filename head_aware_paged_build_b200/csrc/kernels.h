@@ -158,6 +158,7 @@ cudaError_t launch_block_mass(const BlockMassLaunch& a, cudaStream_t s);
 // context lengths in the table (tree_common.cuh): the launch only says how a
 // kernel tiles its rows.
 constexpr int kTreeMaxCtas = 2 * 148 + 24;  // a multiple of 32
+constexpr int kTreeHeadsHere = 64;          // most heads of a call that joins its split groups itself
 // A row group whose pieces lie in several CTAs, kept by the one it starts in:
 // piece 0 is in slot first_slot, piece i in slot 2 (first CTA + i).
 struct alignas(16) TreeJoin {
@@ -193,6 +194,7 @@ struct TreeLaunch {
   int32_t n_ctas;
   float* partial;     // workspace slots, two for each CTA
   TreeJoin* joins;    // workspace, one for each CTA
+  int32_t* tickets;   // workspace, kMaxTreeNodes a head, zero between calls; null: the joining kernel follows
   int32_t* status;
 };
 // How a kernel tiles a call: which kernel, its row group and its grid.
@@ -202,6 +204,7 @@ struct TreeConfig {
   int32_t nodes_per_tile;
   int32_t rows_per_group;  // nodes_per_group * group
   int32_t n_ctas;
+  bool joins_here;  // a short call: the CTA of a group's last piece joins it, and no second kernel is launched
 };
 TreeConfig tree_config(const sp_plan* plan, int32_t nodes);
 cudaError_t launch_tree(const TreeLaunch& a, const TreeConfig& c, cudaStream_t s);

@@ -46,10 +46,13 @@ struct TreeMma {
   static_assert(kMlOff % 8 == 0 && kQOff % 16 == 0 && kDescOff % 16 == 0 && kBarOff % 8 == 0 && kScanOff % 8 == 0 &&
                     kInfoOff % alignof(Info) == 0,
                 "alignment of the shared-memory parts");
-  static constexpr int kBytes = kInfoOff + 2 * int(sizeof(Info));
+  static_assert(alignof(TreeJoinsHere) <= alignof(Info), "the list behind the pieces");
+  static constexpr int kBytes = kInfoOff + 2 * int(sizeof(Info)) + int(sizeof(TreeJoinsHere));
 };
 
-template <int D, bool FP8, int WR, int WT>
+// HERE: the CTAs join split groups themselves (tree_joins_here).  A form of its
+// own: the join's registers cost the page loop of long calls 5 to 9 %.
+template <int D, bool FP8, int WR, int WT, bool HERE>
 __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 : 2) tree_mma_kernel(TreeLaunch a) {
   using C = TreeMma<D, FP8, WR, WT>;
   using Split = typename C::Split;
@@ -68,9 +71,11 @@ __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 
   uint64_t *empty = full + NST, *piece_full = empty + NST, *piece_free = piece_full + 2, *draft_go = piece_free + 2;
   int64_t* scratch = reinterpret_cast<int64_t*>(smem + C::kScanOff);
   Info* info = reinterpret_cast<Info*>(smem + C::kInfoOff);
+  TreeJoinsHere* here = reinterpret_cast<TreeJoinsHere*>(info + 2);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
+    here->n = 0;
     for (int s = 0; s < NST; ++s) {
       mbar_init(&full[s], 1 + ND);  // the producer and the draft's writers (it arrives for them on cached pages)
       mbar_init(&empty[s], NC);
@@ -469,10 +474,18 @@ __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 
         }
       }
     }
-    if (threadIdx.x == 0) tree_note_join(a, pc);
+    if constexpr (!HERE) {
+      if (threadIdx.x == 0) tree_note_join(a, pc);
+    } else if (pc.n_pieces > 1) {
+      __threadfence();
+      bar();
+      if (threadIdx.x == 0) tree_take_ticket(a, pc, here);
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive(&piece_free[ps]);
   }
+  // (the loop ended behind a barrier: every thread sees the list)
+  if constexpr (HERE) tree_join_here<__nv_bfloat16, D>(a, *here, threadIdx.x, NC * 32);
 }
 
 // ---------------------------------------------------------------------------
@@ -498,7 +511,7 @@ __device__ __forceinline__ float dot4(float4 a, float4 b, float s) {
   return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, s))));
 }
 
-template <int D, int P>
+template <int D, int P, bool HERE>
 __global__ void __launch_bounds__(kF32Threads) tree_f32_kernel(TreeLaunch a) {
   using Split = TreeSplit<1, 4, 2>;
   using C = TreeF32<D, P>;
@@ -513,7 +526,9 @@ __global__ void __launch_bounds__(kF32Threads) tree_f32_kernel(TreeLaunch a) {
   __shared__ int64_t scratch[kF32Threads / 32 + 2];
   __shared__ int pos[kF32Rows];
   __shared__ uint64_t anc[kF32Rows];
+  __shared__ TreeJoinsHere here;
   const int tid = threadIdx.x, G = a.group;
+  if (tid == 0) here.n = 0;
   Split split;
   if (!split.template init<kF32Threads>(a, scratch)) return;
   typename Split::Walk walk = split.walk();
@@ -664,31 +679,48 @@ __global__ void __launch_bounds__(kF32Threads) tree_f32_kernel(TreeLaunch a) {
         if (col == 0) slot[rows_max * D + 2 * r] = M, slot[rows_max * D + 2 * r + 1] = L;
       }
     }
-    if (tid == 0) tree_note_join(a, pc);
+    if constexpr (!HERE) {
+      if (tid == 0) tree_note_join(a, pc);
+    } else if (pc.n_pieces > 1) {
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) tree_take_ticket(a, pc, &here);
+    }
+  }
+  if constexpr (HERE) {
+    __syncthreads();
+    tree_join_here<float, D>(a, here, tid, kF32Threads);
   }
 }
 
-template <int D, bool FP8, int WR, int WT>
+template <int D, bool FP8, int WR, bool HERE>
 cudaError_t launch_mma(const TreeLaunch& a, cudaStream_t s) {
-  using C = TreeMma<D, FP8, WR, WT>;
-  const cudaError_t e = allow_smem<tree_mma_kernel<D, FP8, WR, WT>>(C::kBytes);
+  using C = TreeMma<D, FP8, WR, 4>;
+  const cudaError_t e = allow_smem<tree_mma_kernel<D, FP8, WR, 4, HERE>>(C::kBytes);
   if (e != cudaSuccess) return e;
-  tree_mma_kernel<D, FP8, WR, WT><<<a.n_ctas, C::kThreads, C::kBytes, s>>>(a);
+  tree_mma_kernel<D, FP8, WR, 4, HERE><<<a.n_ctas, C::kThreads, C::kBytes, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <int D, int P, bool HERE>
+cudaError_t launch_f32_form(const TreeLaunch& a, cudaStream_t s) {
+  constexpr int bytes = TreeF32<D, P>::kBytes;
+  const cudaError_t e = allow_smem<tree_f32_kernel<D, P, HERE>>(bytes);
+  if (e != cudaSuccess) return e;
+  tree_f32_kernel<D, P, HERE><<<a.n_ctas, kF32Threads, bytes, s>>>(a);
   return cudaGetLastError();
 }
 
 template <int D, int P>
 cudaError_t launch_f32(const TreeLaunch& a, cudaStream_t s) {
-  constexpr int bytes = TreeF32<D, P>::kBytes;
-  const cudaError_t e = allow_smem<tree_f32_kernel<D, P>>(bytes);
-  if (e != cudaSuccess) return e;
-  tree_f32_kernel<D, P><<<a.n_ctas, kF32Threads, bytes, s>>>(a);
-  return cudaGetLastError();
+  return a.tickets ? launch_f32_form<D, P, true>(a, s) : launch_f32_form<D, P, false>(a, s);
 }
 
 template <int D, bool FP8>
 cudaError_t launch_rows(const TreeLaunch& a, cudaStream_t s) {
-  return a.nodes_per_group * a.group <= 16 ? launch_mma<D, FP8, 1, 4>(a, s) : launch_mma<D, FP8, 2, 4>(a, s);
+  if (a.nodes_per_group * a.group <= 16)
+    return a.tickets ? launch_mma<D, FP8, 1, true>(a, s) : launch_mma<D, FP8, 1, false>(a, s);
+  return a.tickets ? launch_mma<D, FP8, 2, true>(a, s) : launch_mma<D, FP8, 2, false>(a, s);
 }
 
 }  // namespace
@@ -696,6 +728,23 @@ cudaError_t launch_rows(const TreeLaunch& a, cudaStream_t s) {
 // Rows of a group: 16 or 32 while a sequence's rows fit; more rows of 16-bit and
 // E4M3 pages go to the tensor cores (kernels_tree_tc.cu) in tiles of 128, two at
 // a time where a sequence has more.  fp32 pages: 16.
+// A call of few heads and few pieces joins its split groups itself: the CTA of a
+// group's last piece reads the others' from L2 in less time than a second launch
+// takes (one user, 5 nodes, group 4, bf16: 13.7 us against 15.3 at 400 tokens,
+// 15.9 against 17.4 at 1600; 64 heads, 8 nodes, 1600 tokens: 17.7 against 20.7).
+// Groups are split at two units or more (TreeSplit's MIN_UNITS), so a head of n
+// pages makes at most n / 2 + 2 pieces a group: up to 16, four batches of loads;
+// beyond, the rows are shared out over the GPU.  With more heads the CTAs have
+// pages enough that the page loop's registers count (128 heads, 1000 tokens:
+// 28.0 us against 27.1).
+constexpr int kPiecesHere = 16;
+static bool tree_joins_here(const sp_plan* plan) {
+  if (plan->hdr.n_heads > kTreeHeadsHere) return false;
+  int32_t most = 0;
+  for (const HeadDesc& h : plan->heads) most = std::max(most, h.n_vpages);
+  const int draft = (kMaxTreeNodes + plan->prob.page_size - 1) / plan->prob.page_size;
+  return (most + draft) / 2 + 2 <= kPiecesHere;
+}
 TreeConfig tree_config(const sp_plan* plan, int32_t nodes) {
   const int g = plan->group, all = nodes * g;
   TreeConfig c{};
@@ -712,6 +761,7 @@ TreeConfig tree_config(const sp_plan* plan, int32_t nodes) {
   }
   c.nodes_per_group = std::min(most, nodes);
   c.rows_per_group = c.nodes_per_group * g;
+  c.joins_here = !c.tensor && tree_joins_here(plan);
   return c;
 }
 

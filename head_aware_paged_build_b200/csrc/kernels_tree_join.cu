@@ -1,9 +1,5 @@
 // Joining the pieces of row groups that tree attention split over CTAs.
 //
-// With m_i, l_i, acc_i the running maximum (log2 domain), sum and unnormalised
-// output of piece i:  M = max m_i,  O = sum 2^(m_i - M) acc_i / sum 2^(m_i - M) l_i,
-// in an order that the pieces' numbers fix, so the same inputs give the same bits.
-//
 // A programmatic dependent launch: its blocks are placed while the attention's
 // last CTAs run and wait for that grid on the device.  (The last CTA of a row
 // group joining it instead was 3 to 10 times slower on the 8K and 32K layers:
@@ -11,8 +7,7 @@
 // block lists the split groups (the CTA a group starts in left its description)
 // and takes its share of items.  A thread holds a row's 16 columns over a part
 // of the pieces; a group of many pieces is divided into 4 or 16 parts, which
-// meet in shared memory.  Bound by L2 latency: a thread asks for kBatch pieces
-// (maximum, sum and columns) at once and rescales once a batch.
+// meet in shared memory.  Bound by L2 latency.
 #include "kernels.h"
 #include "tree_common.cuh"
 
@@ -20,12 +15,11 @@ namespace sp {
 namespace {
 
 constexpr int kJoinThreads = 256;
-constexpr int kBatch = 4;
-constexpr int kCols = 16;
+constexpr int kCols = kJoinCols;
 
 // Parts a group's pieces are divided into: one while a batch holds them.
 __device__ __forceinline__ int join_parts(int n_pieces) {
-  return n_pieces <= kBatch ? 1 : n_pieces <= 4 * kBatch ? 4 : 16;
+  return n_pieces <= kJoinBatch ? 1 : n_pieces <= 4 * kJoinBatch ? 4 : 16;
 }
 
 template <typename T, int D>
@@ -67,8 +61,6 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeLaunch a) {
     for (int i = 0; i < PER; ++i) s_end[lane * PER + i] = items[i] + upto - sum;
   }
   __syncthreads();
-  const int rows_max = a.nodes_per_group * a.group;
-  const int64_t stride = tree_slot_floats(a);
   const int total = s_end[a.n_ctas - 1];
   for (int item = blockIdx.x; item < total; item += gridDim.x) {
     int lo = 0, hi = a.n_ctas - 1;  // the first CTA whose items reach past this one
@@ -82,66 +74,11 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(TreeLaunch a) {
     const int row0 = (item - (lo ? s_end[lo - 1] : 0)) * R;
     // thread = (part, column group, row of the item)
     const int row = row0 + tid % R, cg = tid / R % CG, part = tid / (R * CG);
-    float m = -INFINITY, l = 0.f, acc[kCols];
-#pragma unroll
-    for (int e = 0; e < kCols; ++e) acc[e] = 0.f;
-    if (row < jn.rows) {
-      for (int i0 = part; i0 < jn.n_pieces; i0 += kBatch * parts) {
-        float2 ml[kBatch];
-        float4 x[kBatch][kCols / 4];
-        float top = m;
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          const int i = i0 + u * parts;
-          ml[u] = make_float2(-INFINITY, 0.f);
-          if (i >= jn.n_pieces) continue;
-          const float* s = a.partial + int64_t(i == 0 ? jn.first_slot : 2 * (lo + i)) * stride;
-          ml[u] = __ldcg(reinterpret_cast<const float2*>(s + rows_max * D + 2 * row));
-#pragma unroll
-          for (int c = 0; c < kCols / 4; ++c)
-            x[u][c] = __ldcg(reinterpret_cast<const float4*>(s + tree_acc_at(row, cg * kCols + 4 * c, rows_max)));
-        }
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) top = fmaxf(top, ml[u].x);
-        const float base = top == -INFINITY ? 0.f : top, f0 = exp2f(m - base);
-        m = top;
-        l *= f0;
-#pragma unroll
-        for (int e = 0; e < kCols; ++e) acc[e] *= f0;
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          if (i0 + u * parts >= jn.n_pieces) continue;
-          const float f = exp2f(ml[u].x - base);
-          l += f * ml[u].y;
-#pragma unroll
-          for (int c = 0; c < kCols / 4; ++c) {
-            acc[4 * c] += f * x[u][c].x, acc[4 * c + 1] += f * x[u][c].y;
-            acc[4 * c + 2] += f * x[u][c].z, acc[4 * c + 3] += f * x[u][c].w;
-          }
-        }
-      }
-    }
-    auto out_row = [&](int r) {
-      return (int64_t(jn.b) * a.T + jn.node0 + r / a.group) * a.num_q_heads + jn.kv * a.group + r % a.group;
-    };
+    float m = -INFINITY, l = 0.f, acc[kCols] = {};
+    if (row < jn.rows) tree_sum_pieces<D>(a, jn.n_pieces, jn.first_slot, lo, row, cg, part, parts, m, l, acc);
+    auto out_row = [&](int r) { return tree_out_row(a, jn.b, jn.kv, jn.node0, r); };
     if (parts == 1) {
-      if (row >= jn.rows) continue;
-      const int64_t at = out_row(row);
-      const float inv = a.v_scale / l;
-      T* dst = static_cast<T*>(a.out) + at * D + cg * kCols;
-      if constexpr (sizeof(T) == 2) {
-#pragma unroll
-        for (int e = 0; e < kCols; e += 8)
-          reinterpret_cast<uint4*>(dst)[e / 8] = make_uint4(
-              pack_bf16x2(acc[e] * inv, acc[e + 1] * inv), pack_bf16x2(acc[e + 2] * inv, acc[e + 3] * inv),
-              pack_bf16x2(acc[e + 4] * inv, acc[e + 5] * inv), pack_bf16x2(acc[e + 6] * inv, acc[e + 7] * inv));
-      } else {
-#pragma unroll
-        for (int e = 0; e < kCols; e += 4)
-          reinterpret_cast<float4*>(dst)[e / 4] =
-              make_float4(acc[e] * inv, acc[e + 1] * inv, acc[e + 2] * inv, acc[e + 3] * inv);
-      }
-      if (cg == 0 && a.lse) a.lse[at] = (m + log2f(l)) * kTreeLn2;
+      if (row < jn.rows) tree_finish_row<T, D>(a, out_row(row), cg, m, l, acc);
       continue;
     }
     // the parts meet: each brings its sums to the common maximum, then a thread adds up single columns in order

@@ -399,4 +399,113 @@ __device__ __forceinline__ void tree_note_join(const TreeLaunch& a, const Piece&
       TreeJoin{pc.n_pieces, pc.first_slot, pc.nodes * a.group, pc.hd.b, pc.hd.kv, pc.node0, {0, 0}};
 }
 
+// ---- joining pieces ---------------------------------------------------------
+// With m_i, l_i, acc_i the running maximum (log2 domain), sum and unnormalised
+// output of piece i:  M = max m_i,  O = sum 2^(m_i - M) acc_i / sum 2^(m_i - M) l_i,
+// in an order that the pieces' numbers fix, so the same inputs give the same bits.
+constexpr int kJoinBatch = 4;  // pieces a thread asks for at once
+constexpr int kJoinCols = 16;  // columns of a thread
+
+// Pieces part, part + parts, ... of a row's columns 16 cg ...: a batch's loads go out together, one rescale a batch.
+template <int D>
+__device__ __forceinline__ void tree_sum_pieces(const TreeLaunch& a, int n_pieces, int first_slot, int first_cta,
+                                                int row, int cg, int part, int parts, float& m, float& l,
+                                                float (&acc)[kJoinCols]) {
+  const int rows_max = a.nodes_per_group * a.group;
+  const int64_t stride = tree_slot_floats(a);
+  m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int e = 0; e < kJoinCols; ++e) acc[e] = 0.f;
+  for (int i0 = part; i0 < n_pieces; i0 += kJoinBatch * parts) {
+    float2 ml[kJoinBatch];
+    float4 x[kJoinBatch][kJoinCols / 4];
+    float top = m;
+#pragma unroll
+    for (int u = 0; u < kJoinBatch; ++u) {
+      const int i = i0 + u * parts;
+      ml[u] = make_float2(-INFINITY, 0.f);
+      if (i >= n_pieces) continue;
+      const float* s = a.partial + int64_t(i == 0 ? first_slot : 2 * (first_cta + i)) * stride;
+      ml[u] = __ldcg(reinterpret_cast<const float2*>(s + rows_max * D + 2 * row));
+#pragma unroll
+      for (int c = 0; c < kJoinCols / 4; ++c)
+        x[u][c] = __ldcg(reinterpret_cast<const float4*>(s + tree_acc_at(row, cg * kJoinCols + 4 * c, rows_max)));
+    }
+#pragma unroll
+    for (int u = 0; u < kJoinBatch; ++u) top = fmaxf(top, ml[u].x);
+    const float base = top == -INFINITY ? 0.f : top, f0 = exp2f(m - base);
+    m = top;
+    l *= f0;
+#pragma unroll
+    for (int e = 0; e < kJoinCols; ++e) acc[e] *= f0;
+#pragma unroll
+    for (int u = 0; u < kJoinBatch; ++u) {
+      if (i0 + u * parts >= n_pieces) continue;
+      const float f = exp2f(ml[u].x - base);
+      l += f * ml[u].y;
+#pragma unroll
+      for (int c = 0; c < kJoinCols / 4; ++c) {
+        acc[4 * c] += f * x[u][c].x, acc[4 * c + 1] += f * x[u][c].y;
+        acc[4 * c + 2] += f * x[u][c].z, acc[4 * c + 3] += f * x[u][c].w;
+      }
+    }
+  }
+}
+
+// Output row of row `row` of a group that starts at node node0 of (b, kv).
+__device__ __forceinline__ int64_t tree_out_row(const TreeLaunch& a, int b, int kv, int node0, int row) {
+  return (int64_t(b) * a.T + node0 + row / a.group) * a.num_q_heads + kv * a.group + row % a.group;
+}
+// A finished row's columns 16 cg ..., and with the first of them its LSE.
+template <typename T, int D>
+__device__ __forceinline__ void tree_finish_row(const TreeLaunch& a, int64_t at, int cg, float m, float l,
+                                                const float (&acc)[kJoinCols]) {
+  const float inv = a.v_scale / l;
+  T* dst = static_cast<T*>(a.out) + at * D + cg * kJoinCols;
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int e = 0; e < kJoinCols; e += 8)
+      reinterpret_cast<uint4*>(dst)[e / 8] = make_uint4(
+          pack_bf16x2(acc[e] * inv, acc[e + 1] * inv), pack_bf16x2(acc[e + 2] * inv, acc[e + 3] * inv),
+          pack_bf16x2(acc[e + 4] * inv, acc[e + 5] * inv), pack_bf16x2(acc[e + 6] * inv, acc[e + 7] * inv));
+  } else {
+#pragma unroll
+    for (int e = 0; e < kJoinCols; e += 4)
+      reinterpret_cast<float4*>(dst)[e / 4] =
+          make_float4(acc[e] * inv, acc[e + 1] * inv, acc[e + 2] * inv, acc[e + 3] * inv);
+  }
+  if (cg == 0 && a.lse) a.lse[at] = (m + log2f(l)) * kTreeLn2;
+}
+
+// Short calls (TreeLaunch::tickets): the CTA that publishes a group's last piece
+// joins it, behind its own pieces, of which two at most are parts of a group.
+struct TreeJoinsHere {
+  int n;
+  int first_cta[2];
+  TreeJoin join[2];
+};
+// One thread, behind a fence and a barrier of the block's stores; also returns the counter to zero.
+template <typename Piece>
+__device__ __forceinline__ void tree_take_ticket(const TreeLaunch& a, const Piece& pc, TreeJoinsHere* here) {
+  int32_t* c = a.tickets + int64_t(pc.head) * kMaxTreeNodes + pc.group;
+  if (atomicAdd(c, 1) != pc.n_pieces - 1) return;
+  *c = 0;
+  const int i = here->n++;
+  here->first_cta[i] = pc.first_cta;
+  here->join[i] = TreeJoin{pc.n_pieces, pc.first_slot, pc.nodes * a.group, pc.hd.b, pc.hd.kv, pc.node0, {0, 0}};
+}
+template <typename T, int D>
+__device__ __forceinline__ void tree_join_here(const TreeLaunch& a, const TreeJoinsHere& here, int tid, int threads) {
+  __threadfence();
+  for (int i = 0; i < here.n; ++i) {
+    const TreeJoin& jn = here.join[i];
+    for (int e = tid; e < jn.rows * (D / kJoinCols); e += threads) {
+      const int row = e % jn.rows, cg = e / jn.rows;
+      float m, l, acc[kJoinCols];
+      tree_sum_pieces<D>(a, jn.n_pieces, jn.first_slot, here.first_cta[i], row, cg, 0, 1, m, l, acc);
+      tree_finish_row<T, D>(a, tree_out_row(a, jn.b, jn.kv, jn.node0, row), cg, m, l, acc);
+    }
+  }
+}
+
 }  // namespace sp

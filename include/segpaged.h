@@ -466,13 +466,15 @@ SP_API sp_status segpaged_decode_step(const sp_plan* plan, void* d_table, const 
  *            draft, parents) and are not written
  *   softmax_scale  <= 0 selects 1/sqrt(head_dim)
  *   workspace device, 256-byte aligned, at least what segpaged_tree_workspace
- *            gives for `nodes` or more.  It begins with a status block of its
- *            own (segpaged_read_device_status), zero before the first use.
+ *            gives for `nodes` or more, zero-filled before its first use.  It
+ *            begins with a status block of its own (segpaged_read_device_status)
+ *            and holds counters that the kernels return to zero: after a device
+ *            status of a wait that ran out, zero it again before reuse.
  *            Calls that overlap on the GPU need separate workspaces.
- * All decode plans, ring plans or not, every dtype and page type.  Two launches
- * on `stream` (the attention, and a programmatic dependent of it that joins rows
- * split over the GPU); fixed summation orders: the same inputs give the same
- * bits.  A parent not in [-1, i), or a num_nodes outside [0, nodes], is found
+ * All decode plans, ring plans or not, every dtype and page type.  One or two
+ * launches on `stream` (the attention, and where rows are split over much of the
+ * GPU a programmatic dependent that joins them); fixed summation orders: the same
+ * inputs give the same bits.  A parent not in [-1, i), or a num_nodes outside [0, nodes], is found
  * on the device: status code 8; the node then counts as a root, the count as
  * the nearest one in range. */
 SP_API sp_status segpaged_tree_workspace(const sp_plan* plan, int32_t max_nodes, size_t* bytes);

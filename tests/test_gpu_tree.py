@@ -165,6 +165,30 @@ def test_pieces_of_one_and_two_tiles_repeat_bit_for_bit(pages, d, T, g):
     assert case.layer.device_status() == 0
 
 
+@pytest.mark.parametrize("pages,d", [("bf16", 128), ("e4m3", 64), ("f32", 128)])
+def test_short_calls_of_changing_sizes_share_a_workspace(pages, d):
+    """Few heads over few pages join their pieces by counters that one call leaves ready for the next."""
+    case = Case(pages, d, 2, 16, (1500, 700), hkv=4, policy=[("global", 0, 0), ("local", 4, 600)])
+    case.check()
+    ones = torch.full((2,), 1, dtype=torch.int32, device="cuda")
+    first = {}
+    for turn in range(40):
+        for t in (16, 1, 5, 8, 13):
+            out, lse = torch.zeros_like(case.q[:, :t]), torch.zeros(2, t, 8, device="cuda")
+            case.layer.tree_attention(case.q[:, :t].contiguous(), case.kd[:, :t].contiguous(),
+                                      case.vd[:, :t].contiguous(), case.par[:, :t].contiguous(),
+                                      num_nodes=ones * min(t, 1 + turn % 3), out=out, lse=lse)
+            o, l = first.setdefault((t, turn % 3), (out, lse))
+            assert torch.equal(o, out) and torch.equal(l, lse), (turn, t)
+    assert case.layer.device_status() == 0
+    want = case.call()[0]
+    for t in (5, 13):  # a node's result does not depend on the nodes behind it
+        out = case.layer.tree_attention(case.q[:, :t].contiguous(), case.kd[:, :t].contiguous(),
+                                        case.vd[:, :t].contiguous(), case.par[:, :t].contiguous())[0]
+        tol = 1e-5 if pages == "f32" else 2e-2
+        assert torch.allclose(out.float(), want[:, :t].float(), rtol=tol, atol=tol)
+
+
 def test_more_heads_than_threads():
     lens = [random.Random(5).randint(1, 200) for _ in range(70)]
     Case("bf16", 64, 2, 6, lens, [n % 7 for n in lens], hkv=9).check()
