@@ -199,7 +199,7 @@ struct TreeLaunch {
 };
 // How a kernel tiles a call: which kernel, its row group and its grid.
 struct TreeConfig {
-  bool tensor;  // the tcgen05 kernel (bf16 pages)
+  bool tensor;  // the tcgen05 kernel
   int32_t nodes_per_group;
   int32_t nodes_per_tile;
   int32_t rows_per_group;  // nodes_per_group * group

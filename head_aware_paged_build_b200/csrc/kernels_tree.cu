@@ -725,9 +725,6 @@ cudaError_t launch_rows(const TreeLaunch& a, cudaStream_t s) {
 
 }  // namespace
 
-// Rows of a group: 16 or 32 while a sequence's rows fit; more rows of 16-bit and
-// E4M3 pages go to the tensor cores (kernels_tree_tc.cu) in tiles of 128, two at
-// a time where a sequence has more.  fp32 pages: 16.
 // A call of few heads and few pieces joins its split groups itself: the CTA of a
 // group's last piece reads the others' from L2 in less time than a second launch
 // takes (one user, 5 nodes, group 4, bf16: 13.7 us against 15.3 at 400 tokens,
@@ -745,6 +742,10 @@ static bool tree_joins_here(const sp_plan* plan) {
   const int draft = (kMaxTreeNodes + plan->prob.page_size - 1) / plan->prob.page_size;
   return (most + draft) / 2 + 2 <= kPiecesHere;
 }
+
+// Rows of a group: 16 or 32 while a sequence's rows fit; more rows of 16-bit and
+// E4M3 pages go to the tensor cores (kernels_tree_tc.cu) in tiles of 128, two at
+// a time where a sequence has more.  fp32 pages: 16.
 TreeConfig tree_config(const sp_plan* plan, int32_t nodes) {
   const int g = plan->group, all = nodes * g;
   TreeConfig c{};

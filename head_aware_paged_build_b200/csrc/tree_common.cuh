@@ -18,7 +18,7 @@
 // slot each of them wrote (its first piece: 2c, a later one: 2c + 1; pieces
 // between cover their group and need none) are arithmetic on (U, G).  A group
 // in one CTA is written there; the others' pieces are joined by a second,
-// dependent kernel.
+// dependent kernel, or in short calls by the CTA of a group's last piece.
 #pragma once
 
 #include "append_common.cuh"

@@ -195,8 +195,10 @@ class SegPagedLayer:
 
         A call makes it when it is missing; a CUDA graph capture needs it made before.  Workspaces
         that a larger one replaced are kept: a captured graph may hold their addresses."""
-        if max_nodes <= self.tree_nodes:
+        if 1 <= max_nodes <= self.tree_nodes:
             return
+        if 1 <= max_nodes <= S.SP_TREE_MAX_NODES:  # trees that grow node by node need few workspaces
+            max_nodes = (max_nodes + 15) // 16 * 16
         need = S.segpaged_tree_workspace(self.plan, max_nodes)
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("call prepare_tree(max_nodes) before a CUDA graph capture")

@@ -474,9 +474,9 @@ SP_API sp_status segpaged_decode_step(const sp_plan* plan, void* d_table, const 
  * All decode plans, ring plans or not, every dtype and page type.  One or two
  * launches on `stream` (the attention, and where rows are split over much of the
  * GPU a programmatic dependent that joins them); fixed summation orders: the same
- * inputs give the same bits.  A parent not in [-1, i), or a num_nodes outside [0, nodes], is found
- * on the device: status code 8; the node then counts as a root, the count as
- * the nearest one in range. */
+ * inputs give the same bits.  A parent not in [-1, i), or a num_nodes outside
+ * [0, nodes], is found on the device: status code 8; the node then counts as a
+ * root, the count as the nearest one in range. */
 SP_API sp_status segpaged_tree_workspace(const sp_plan* plan, int32_t max_nodes, size_t* bytes);
 SP_API sp_status segpaged_tree_attention(const sp_plan* plan, const void* d_table, const void* k_pool,
                                          const void* v_pool, const void* q, const void* k_draft, const void* v_draft,

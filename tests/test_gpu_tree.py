@@ -265,6 +265,18 @@ def test_trees_of_other_sizes_share_a_workspace():
     assert len(big.layer.tree_workspaces) == 1
 
 
+def test_workspaces_of_growing_trees():
+    layer = Case("bf16", 64, 2, 3, (100, 5), hkv=2, policy=MIXED[:2]).layer
+    for bad in (0, -1, 65):
+        with pytest.raises(S.SegPagedError):
+            layer.prepare_tree(bad)
+    for n in range(1, 65):
+        layer.prepare_tree(n)
+        assert layer.tree_nodes >= n
+        assert layer.tree_workspaces[-1].numel() >= S.segpaged_tree_workspace(layer.plan, n)
+    assert len(layer.tree_workspaces) <= 4
+
+
 def test_bad_trees_are_reported():
     """A parent at or behind its node counts as a root, a node count out of range as the nearest one in range."""
     c = Case("bf16", 128, 2, 6, (70, 200, 9), (6, 6, 6), hkv=2, policy=MIXED[:2])
