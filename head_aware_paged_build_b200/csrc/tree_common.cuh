@@ -162,50 +162,43 @@ template <int D, DraftForm FORM>
 __device__ __forceinline__ void tree_draft_v(const TreeLaunch& a, const HeadDesc& hd, int n, uint8_t* vdst, int lane) {
   const __nv_bfloat16* vn =
       static_cast<const __nv_bfloat16*>(a.v_draft) + int64_t(hd.b) * a.ds_seq + int64_t(hd.kv) * a.ds_head;
-  // a lane takes two dimensions of a run of tokens and writes a 16-byte chunk of each
+  // A lane takes two dimensions of eight positions and writes a chunk of each, two such runs at a time: the loads'
+  // latency counts (24 nodes over 64 heads: 47 us, one at a time 56).  In the E4M3 tcgen05 form, whose roles fill the
+  // instruction cache, code that runs once or twice a CTA has to be short: one at a time its 32K layer takes 85 us, two
+  // runs of sixteen positions 105.
   constexpr bool FP8 = FORM != kDraftBf16;
-  constexpr int DP = D / 2, TG = FP8 ? 16 : 8;
-#pragma unroll 2
-  for (int u = lane; u < DP * (64 / TG); u += 32) {
+  constexpr int DP = D / 2;
+#pragma unroll(FORM == kDraftWide ? 1 : 2)
+  for (int u = lane; u < DP * 8; u += 32) {
     const int i = (u % DP) * 2, g = u / DP;
-    uint32_t x[TG];
+    const int t0 = FP8 ? (g >> 1) * 16 + (g & 1) * 4 : g * 8;  // E4M3: positions 8 ... 15 of 16 are 4 tokens behind
+    uint32_t x[8];
 #pragma unroll
-    for (int e = 0; e < TG; ++e) {
-      const int t = g * TG + (FP8 ? fp8_vpos_tok(e) : e);
+    for (int e = 0; e < 8; ++e) {
+      const int t = t0 + (FP8 ? fp8_vpos_tok(e) : e);
       x[e] = t < n ? *reinterpret_cast<const uint32_t*>(vn + t * a.ds_tok + i) : 0u;
     }
-    uint32_t lo[4], hi[4];  // dimension i, dimension i + 1
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      if constexpr (FP8) {
-        uint32_t c[2] = {0, 0};
+    for (int y = 0; y < 2; ++y) {  // dimension i, dimension i + 1
+      uint32_t w[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t p = x[4 * w + 2 * h], r = x[4 * w + 2 * h + 1];
-          c[0] |= uint32_t(pack_e4m3x2(__uint_as_float(p << 16) * a.v_inv, __uint_as_float(r << 16) * a.v_inv))
-                  << (16 * h);
-          c[1] |= uint32_t(pack_e4m3x2(__uint_as_float(p & 0xffff0000u) * a.v_inv,
-                                       __uint_as_float(r & 0xffff0000u) * a.v_inv))
-                  << (16 * h);
-        }
-        lo[w] = c[0], hi[w] = c[1];
-      } else {
-        lo[w] = __byte_perm(x[2 * w], x[2 * w + 1], 0x5410);
-        hi[w] = __byte_perm(x[2 * w], x[2 * w + 1], 0x7632);
+      for (int h = 0; h < 4; ++h) {
+        const uint32_t p = x[2 * h], r = x[2 * h + 1];
+        if constexpr (FP8)
+          w[h] = pack_e4m3x2(__uint_as_float(y ? p & 0xffff0000u : p << 16) * a.v_inv,
+                             __uint_as_float(y ? r & 0xffff0000u : r << 16) * a.v_inv);
+        else
+          w[h] = __byte_perm(p, r, y ? 0x7632 : 0x5410);
       }
-    }
-#pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      const uint32_t(&w)[4] = y ? hi : lo;
-      if constexpr (FORM == kDraftWide) {
-        uint4 o[2];
-        widen16(make_uint4(w[0], w[1], w[2], w[3]), o[0], o[1]);
-        *reinterpret_cast<uint4*>(vdst + vpage_chunk_offset_bf16(i + y, 2 * g)) = o[0];
-        *reinterpret_cast<uint4*>(vdst + vpage_chunk_offset_bf16(i + y, 2 * g + 1)) = o[1];
-      } else {
-        const int64_t at = FP8 ? fp8_vpage_offset(i + y, g * 16) : vpage_chunk_offset_bf16(i + y, g);
-        *reinterpret_cast<uint4*>(vdst + at) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
+      if constexpr (FORM == kDraftE4m3)
+        *reinterpret_cast<uint2*>(vdst + fp8_vpage_offset(i + y, g * 8)) =
+            make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+      else if constexpr (FORM == kDraftWide)
+        *reinterpret_cast<uint4*>(vdst + vpage_chunk_offset_bf16(i + y, g)) =
+            make_uint4(e4m3x2_to_f16x2(uint16_t(w[0])), e4m3x2_to_f16x2(uint16_t(w[1])),
+                       e4m3x2_to_f16x2(uint16_t(w[2])), e4m3x2_to_f16x2(uint16_t(w[3])));
+      else
+        *reinterpret_cast<uint4*>(vdst + vpage_chunk_offset_bf16(i + y, g)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
