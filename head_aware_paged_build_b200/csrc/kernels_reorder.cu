@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kReorderThreads) reorder_kernel(const __grid_c
   for (;;) {
     for (int b = tid; b < B; b += kReorderThreads)
       if (!listed[b] && readers[b] == 0) {
-        listed[b] = 2;  // this round
+        listed[b] = 2;
         moves[atomicAdd(&s_count, 1)] = Move{int16_t(b), from[b], -1, 0};
       }
     __syncthreads();

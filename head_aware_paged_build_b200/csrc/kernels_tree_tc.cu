@@ -102,8 +102,8 @@ struct PageSlots {
 constexpr int32_t kSlotsAll = -1;    // every row sees every slot
 constexpr int32_t kSlotsDraft = -2;  // the draft's page
 
-// E4M3 form: parked, so that its sixteen warps poll less (197 us where this takes 165, before the widening below
-// was made cheaper); the bf16 form is 3 % faster without.
+// E4M3 form: parked, so that its sixteen warps poll less (its 32K layer of 16 nodes takes 85 us, polling 95); the
+// bf16 form is 3 % faster without.
 template <bool PARKED>
 __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity) {
   return PARKED ? mbar_wait_parked(bar, parity) : mbar_wait(bar, parity);
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
         const uint32_t ts = t_s(x, b) + lane_off;
         tc::fence_after_sync();
         // two passes over the scores, which stay in TMEM.  The E4M3 form rolls the halves: unrolled, the loops of its
-        // roles outgrow the instruction cache (207 us where it took 197); the bf16 form is 3 % faster unrolled
+        // roles outgrow the instruction cache (97 us where it takes 85); the bf16 form is 3 % faster unrolled
         float mts = -INFINITY;
 #pragma unroll(FP8 ? 1 : 2)
         for (int c = 0; c < 2; ++c) {
