@@ -251,14 +251,16 @@ sp_status plan_build(sp_plan& pl) {
         // Retrieval: per block, its sink part and its kept part are seen causally
         // by every query; an unkept block keeps only its part inside the calls'
         // windows [max(sink, q0 - w + 1), L).  Touching runs merge when they share
-        // the flag; in decode plans (one query, which sees every stored position)
-        // touching runs always merge.
+        // the flag: drafted tokens stand behind the last position, and see a kept
+        // block where the window has moved on.  For one query a run of nothing but
+        // sink positions joins the next one whatever its flag, since the local rule
+        // shows the sink too.
         const int64_t rec = std::max<int64_t>(s, q0 - w + 1);
         const bool decode_head = q0 == L - 1;
         auto add = [&](int64_t a, int64_t e, bool causal) {
           if (e <= a) return;
           if (!runs.empty() && runs.back().start + runs.back().len == a &&
-              (runs.back().causal == causal || decode_head)) {
+              (runs.back().causal == causal || (decode_head && a <= s))) {
             runs.back().len += e - a;
             runs.back().causal = runs.back().causal && causal;
           } else {

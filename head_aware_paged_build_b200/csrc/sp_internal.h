@@ -50,8 +50,8 @@ constexpr int32_t kNoPage = -1;
 
 // One (sequence, kv-head).  Kinds are resolved: 0 reads the whole causal
 // context, 1 applies the local rule (sink + window) to every page that is not
-// flagged kSpanCausal.  A retrieval head is kind 1 whose sink pages and kept
-// blocks' pages carry that flag.
+// flagged kSpanCausal.  A retrieval head is kind 1 whose kept blocks' pages
+// carry that flag, and its sink's pages where they hold nothing of the window.
 struct alignas(16) HeadDesc {
   int32_t kind;
   int32_t sink;

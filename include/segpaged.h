@@ -208,10 +208,10 @@ typedef struct sp_plan sp_plan;
  * only, no CUDA call.  For each (b, kv): GLOBAL/DENSE keep one segment
  * [0, L); LOCAL keeps [0, min(sink, L)) and [max(sink, q0 - window + 1), L),
  * the union of what the call's queries see (merged when they touch);
- * RETRIEVAL keeps the LOCAL runs plus its kept blocks (in prefill plans a
- * run that every query sees causally, sink or kept blocks, is a segment of
- * its own, apart from the window's runs).  Each segment starts on a fresh
- * page.  The plan also holds the decode split list
+ * RETRIEVAL keeps the LOCAL runs plus its kept blocks (a run that every query
+ * sees causally, sink or kept blocks, is a segment of its own, apart from the
+ * window's runs; where a sequence has one query the sink may join either).
+ * Each segment starts on a fresh page.  The plan also holds the decode split list
  * and the prefill tile list, so that no layout work happens per attention
  * call (same page, §5: layout computed on every call cost a 0.70x slowdown).
  * The plan is immutable and may be shared by several streams. */
