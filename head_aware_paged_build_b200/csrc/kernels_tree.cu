@@ -11,7 +11,8 @@
 // takes 64 / WT of each page's tokens, 16 at a time: S = Q K^T, online softmax
 // with a lazy rescale, O += P V on m16n8k16 fragments.  Scores, sums and O are
 // fp32; P is rounded to the type of the pages' operands (bf16, or f16 over
-// widened E4M3 codes), V's own type, while the sums use the unrounded weights.
+// widened E4M3 codes, lifted: kWeightLift), V's own type, while the sums use the
+// unrounded weights.
 #include <algorithm>
 
 #include "tree_common.cuh"
@@ -61,6 +62,7 @@ __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 
   constexpr int KSTEPS = D / 16, NT = D / 8, CHUNKS = 4 / WT;
   constexpr uint32_t kAll = 0xffffffffu;
   constexpr DraftForm FORM = FP8 ? kDraftE4m3 : kDraftBf16;
+  constexpr float kLift = FP8 ? kWeightLift : 0.f;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* stage = smem;
   float* mbuf = reinterpret_cast<float*>(smem + C::kMergeOff);
@@ -362,7 +364,7 @@ __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 
 #pragma unroll
           for (int j = 0; j < NT; ++j) o[j][0] *= al[0], o[j][1] *= al[0], o[j][2] *= al[1], o[j][3] *= al[1];
         }
-        const float b0 = m[0] == -INFINITY ? 0.f : m[0], b1 = m[1] == -INFINITY ? 0.f : m[1];
+        const float b0 = m[0] == -INFINITY ? 0.f : m[0] - kLift, b1 = m[1] == -INFINITY ? 0.f : m[1] - kLift;
         float pr[2][4];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
@@ -406,6 +408,7 @@ __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 
     for (int x = 0; x < 2; ++x) {
       l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
       l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+      m[x] -= kLift;  // what l and o are relative to
     }
     if constexpr (WT > 1) {
       if (wt > 0) {

@@ -38,7 +38,7 @@
 //              and two warps each widen K and V into the operand rings, once a page,
 //              as f16, which holds every code; Q is rewritten as f16 in place
 // Sums, maxima and O are fp32; P is rounded to the operands' type: bf16, V's own, or
-// f16 over widened codes.
+// f16 over widened codes (lifted: kWeightLift).
 // Every wait is bounded; one that runs out records a status code, and the CTA
 // drains its copies and MMAs, frees its TMEM and returns.
 #include <cuda.h>
@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
   using Info = typename C::Info;
   constexpr int kThreads = C::kThreads;
   constexpr int KS = C::KS, VS = C::VS, RS = C::RS, kUses = WIDE ? 2 : 1;
+  constexpr float kLift = FP8 ? kWeightLift : 0.f;
   // the rings that the copies fill
   constexpr int KR = FP8 ? RS : KS, VR = FP8 ? RS : VS, kCopy = FP8 ? C::kRaw : C::kPage;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -591,7 +592,7 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
             }
           }
         }
-        const float base = m == -INFINITY ? 0.f : m;
+        const float base = m == -INFINITY ? 0.f : m - kLift;
         const uint64_t nbase2 = f2_pack(-base, -base), scale2 = f2_pack(sl2, sl2);
         uint64_t s2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
 #pragma unroll(FP8 ? 1 : 2)
@@ -630,6 +631,7 @@ __global__ void __launch_bounds__(TreeTc<D, WIDE, FP8>::kThreads, 1)
         if (lane == 0) mbar_arrive(&p_full[2 * x + b]);
       }
       // ------------------------------ end of the piece ------------------------------
+      m -= kLift;  // what l and O are relative to
       if (U > 1) phase ^= 1u << 2;
       if (U > 0) {
         wait(&o_done[x], 3);

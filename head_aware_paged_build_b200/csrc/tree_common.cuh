@@ -29,6 +29,13 @@ namespace sp {
 constexpr int kDraftPage = -2;  // phys of the draft's page in a stage's record
 constexpr float kTreeLn2 = 0.6931471805599453f;
 
+// E4M3 pages: softmax weights are f16 operands, taken 2^7 times larger.  The
+// lazy rescale lets a weight reach 2^8 times the running maximum's, so 2^15 of
+// f16's 65504 is used, and a weight's rounding, half a subnormal step of 2^-24,
+// is 2^-32 of the maximum's.  (Without the lift 2^-25: beside a dominant key,
+// 32768 others below that, up to a thousandth of the row together, would vanish.)
+constexpr float kWeightLift = 7.f;
+
 // Bits [x, y) of a 64-bit word (any x, y).
 __device__ __forceinline__ uint64_t bit_range(int x, int y) {
   x = max(x, 0), y = min(y, 64);
