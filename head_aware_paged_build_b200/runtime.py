@@ -237,7 +237,8 @@ class SegPagedLayer:
         earlier node; ``num_nodes``: int32 [B] or None (T each).  Node i at depth d stands at position
         L + d and sees the cache by its head's rule, its ancestors and itself.  Returns (out, lse); rows
         behind ``num_nodes[b]`` are left as they were (in fresh outputs: zero).  T is at most 64.  The
-        layer's calls share its workspaces: they must not overlap on the GPU."""
+        layer's calls share its workspaces: they must not overlap on the GPU.  After a device status of a
+        wait that ran out (codes 1 to 4) call ``clear_device_status`` before the next one."""
         self._check_tensor(q, "q", self.torch_dtype)
         T = q.shape[1] if q.dim() == 4 else 0
         if not 1 <= T <= S.SP_TREE_MAX_NODES or not q.is_contiguous() or \
@@ -316,6 +317,14 @@ class SegPagedLayer:
         for ws in self.tree_workspaces:
             code = code or S.segpaged_read_device_status(ws.data_ptr(), _stream(stream))
         return code
+
+    def clear_device_status(self, stream=None) -> None:
+        """Zero the layer's workspaces: the recorded codes, and the counters that a wait which ran out may have
+        left behind (``segpaged_clear_device_status`` clears the code of one workspace alone).  None of the
+        layer's calls may be running on another stream."""
+        with _on(self.k_pool.device, stream):
+            for ws in (self.workspace, *self.tree_workspaces):
+                ws.zero_()
 
     def close(self) -> None:
         if getattr(self, "plan", None):

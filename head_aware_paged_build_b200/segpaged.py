@@ -339,6 +339,7 @@ def segpaged_read_device_status(workspace: int, stream: int = 0) -> int:
 
 
 def segpaged_clear_device_status(workspace: int, stream: int = 0) -> None:
+    """Zero a workspace's status block alone (after codes 1 to 4 zero the whole workspace instead)."""
     _check(load().segpaged_clear_device_status(workspace, stream), "segpaged_clear_device_status")
 
 

@@ -542,7 +542,9 @@ SP_API sp_status segpaged_reorder(const sp_plan* plan, void* d_table, const int3
  * read synchronises `stream`, copies the word to *code (host) and returns
  * SP_OK for 0, SP_ERR_DEVICE_CHECK for a recorded code (SP_ERR_CUDA if the
  * synchronisation or the copy fails); clear zeroes the word's 256-byte block
- * asynchronously on `stream`.  `workspace` is the one given to the kernels. */
+ * asynchronously on `stream`, and nothing else: after a wait that ran out (1 to
+ * 4) the counters behind it may not be at zero, so zero the whole workspace
+ * instead.  `workspace` is the one given to the kernels. */
 SP_API sp_status segpaged_read_device_status(const void* workspace, int32_t* code, void* stream);
 SP_API sp_status segpaged_clear_device_status(void* workspace, void* stream);
 

@@ -1,0 +1,55 @@
+"""Workspaces of tree attention: what a layer keeps and resets."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from head_aware_paged_build_b200 import segpaged as S
+from test_gpu_tree import MIXED, Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    S.load()
+
+
+def _short_case(**kw):
+    """A call that joins its split rows by counters in the workspace."""
+    return Case("bf16", 128, 2, 8, (1500, 700), hkv=2, policy=MIXED[:2], **kw)
+
+
+def test_clearing_the_status_makes_the_workspaces_fresh():
+    """What a wait that ran out leaves behind: a status code, and counters that were not returned to zero."""
+    c = _short_case()
+    want = [x.clone() for x in c.call()]
+    attended = [x.clone() for x in c.layer.attention(c.q[:, 0].contiguous())]
+    torch.cuda.synchronize()
+    for ws in (c.layer.workspace, *c.layer.tree_workspaces):
+        ws.view(torch.int32)[:6000].fill_(1)
+    assert c.layer.device_status() == 1
+    c.layer.clear_device_status()
+    assert c.layer.device_status() == 0
+    for _ in range(3):
+        got = c.call()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+        got = c.layer.attention(c.q[:, 0].contiguous())
+        assert all(torch.equal(x, y) for x, y in zip(got, attended))
+    assert c.layer.device_status() == 0
+
+
+def test_clearing_the_status_on_a_stream():
+    c = _short_case()
+    want = [x.clone() for x in c.call()]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        c.layer.tree_workspaces[-1].view(torch.int32)[:6000].fill_(1)
+        side.wait_stream(torch.cuda.current_stream())
+        c.layer.clear_device_status(stream=stream)
+        got = c.call(stream=side)
+        side.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    assert c.layer.device_status() == 0
