@@ -200,11 +200,12 @@ class SegPagedLayer:
         if 1 <= max_nodes <= S.SP_TREE_MAX_NODES:  # trees that grow node by node need few workspaces
             max_nodes = (max_nodes + 15) // 16 * 16
         need = S.segpaged_tree_workspace(self.plan, max_nodes)
-        if torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("call prepare_tree(max_nodes) before a CUDA graph capture")
-        device = self.k_pool.device
-        self.tree_workspaces.append(torch.zeros(need, dtype=torch.uint8, device=device))
-        torch.cuda.current_stream(device).synchronize()  # zeroed before any stream's call uses it
+        if not self.tree_workspaces or self.tree_workspaces[-1].numel() < need:  # larger trees may need no more bytes
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("call prepare_tree(max_nodes) before a CUDA graph capture")
+            device = self.k_pool.device
+            self.tree_workspaces.append(torch.zeros(need, dtype=torch.uint8, device=device))
+            torch.cuda.current_stream(device).synchronize()  # zeroed before any stream's call uses it
         self.tree_nodes = max_nodes
 
     def _elsewhere(self, stream) -> bool:

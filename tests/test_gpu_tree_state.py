@@ -53,3 +53,14 @@ def test_clearing_the_status_on_a_stream():
         side.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(got, want))
     assert c.layer.device_status() == 0
+
+
+def test_trees_that_need_no_more_bytes_keep_their_workspace():
+    layer = Case("bf16", 128, 8, 3, (500, 5), hkv=2, policy=MIXED[:2]).layer
+    for n in (20, 33, 48, 64, 17, 64):  # 256 rows a group from 32 nodes on
+        layer.prepare_tree(n)
+        assert layer.tree_workspaces[-1].numel() >= S.segpaged_tree_workspace(layer.plan, n)
+    assert len(layer.tree_workspaces) == 1
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        layer.prepare_tree(64)  # nothing to allocate
+        torch.zeros(1, device="cuda")
