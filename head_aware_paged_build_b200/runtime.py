@@ -190,11 +190,23 @@ class SegPagedLayer:
         return out, lse
 
     # -- several candidates a sequence -------------------------------------------
-    def prepare_tree(self, max_nodes: int) -> None:
-        """Allocate the workspace of ``tree_attention`` for trees of up to ``max_nodes`` nodes.
+    def prepare_tree(self, max_nodes: int, workspace: torch.Tensor | None = None) -> None:
+        """Allocate the workspace of ``tree_attention`` for trees of up to ``max_nodes`` nodes, or take ``workspace``.
 
         A call makes it when it is missing; a CUDA graph capture needs it made before.  Workspaces
-        that a larger one replaced are kept: a captured graph may hold their addresses."""
+        that a larger one replaced are kept: a captured graph may hold their addresses.  Layers whose calls
+        never overlap on the GPU, as those of one model, can use one: ``workspace`` is a zero-filled
+        uint8 tensor, or another layer's ``tree_workspaces[-1]`` (the layers then share its status too)."""
+        if workspace is not None:
+            self._check_tensor(workspace, "workspace", torch.uint8)
+            need = S.segpaged_tree_workspace(self.plan, max_nodes)
+            if not workspace.is_contiguous() or workspace.data_ptr() % 256 or workspace.numel() < need:
+                raise ValueError(f"workspace must be contiguous, 256-byte aligned and hold {need} bytes for "
+                                 f"{max_nodes} nodes, got {workspace.numel()}")
+            if not any(workspace is ws for ws in self.tree_workspaces[-1:]):
+                self.tree_workspaces.append(workspace)
+            self.tree_nodes = max_nodes
+            return
         if 1 <= max_nodes <= self.tree_nodes:
             return
         if 1 <= max_nodes <= S.SP_TREE_MAX_NODES:  # trees that grow node by node need few workspaces

@@ -1,4 +1,4 @@
-"""Workspaces of tree attention: what a layer keeps and resets."""
+"""Workspaces of tree attention: what a layer keeps, resets and shares with others."""
 from __future__ import annotations
 
 import pytest
@@ -64,3 +64,27 @@ def test_trees_that_need_no_more_bytes_keep_their_workspace():
     with torch.cuda.graph(torch.cuda.CUDAGraph()):
         layer.prepare_tree(64)  # nothing to allocate
         torch.zeros(1, device="cuda")
+
+
+@pytest.mark.parametrize("pages", ["bf16", "e4m3", "f32"])
+def test_layers_of_a_model_share_a_workspace(pages):
+    """Layers of other shapes, short calls and split ones, one after another on one workspace."""
+    cases = [Case(pages, 128, 2, 8, (1500, 700), hkv=2, policy=MIXED[:2], seed=1),
+             Case(pages, 64, 4, 16, (9000, 3), hkv=3, policy=MIXED[:3], seed=2),
+             Case(pages, 128, 2, 8, (70, 2000), hkv=2, policy=MIXED[:2], seed=3)]
+    want = [[x.clone() for x in c.call()] for c in cases]
+    need = max(S.segpaged_tree_workspace(c.layer.plan, 16) for c in cases)
+    shared = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for c in cases:
+        c.layer.prepare_tree(16, workspace=shared)
+        c.layer.prepare_tree(16, workspace=shared)
+        assert c.layer.tree_workspaces[-1] is shared and c.layer.tree_nodes == 16
+        c.layer.prepare_tree(9)
+        assert c.layer.tree_workspaces[-1] is shared
+    for _ in range(5):
+        for c, w in zip(cases, want):
+            assert all(torch.equal(x, y) for x, y in zip(c.call(), w))
+    assert all(c.layer.device_status() == 0 for c in cases)
+    cases[0].layer.prepare_tree(64)  # more than it covers: one of its own
+    assert cases[0].layer.tree_workspaces[-1].numel() >= S.segpaged_tree_workspace(cases[0].layer.plan, 64)
