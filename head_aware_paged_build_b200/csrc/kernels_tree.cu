@@ -6,10 +6,10 @@
 // pages into a ring of shared-memory stages with bulk copies, as decode does;
 // one or two more warps write the draft's rows as one more page of the same
 // layout (E4M3 pages: quantised as an append would, so a node sees exactly the
-// codes the cache will hold once the node is committed).  WR x WT consumer
+// codes the cache will hold once the node is committed).  WR x 4 consumer
 // warps: warp (wr, wt) holds rows 16 wr .. 16 wr + 15 of the row group and
-// takes 64 / WT of each page's tokens, 16 at a time: S = Q K^T, online softmax
-// with a lazy rescale, O += P V on m16n8k16 fragments.  Scores, sums and O are
+// takes tokens 16 wt ... of each page: S = Q K^T, online softmax with a lazy
+// rescale, O += P V on m16n8k16 fragments.  Scores, sums and O are
 // fp32; P is rounded to the type of the pages' operands (bf16, or f16 over
 // widened E4M3 codes, lifted: kWeightLift), V's own type, while the sums use the
 // unrounded weights.
@@ -22,8 +22,9 @@ namespace {
 
 constexpr float kLazyLog2 = 8.f;
 
-template <int D, bool FP8, int WR, int WT>
+template <int D, bool FP8, int WR>
 struct TreeMma {
+  static constexpr int WT = 4;  // warps over a page's tokens
   static constexpr int kConsumers = WR * WT;
   // 16-row form: two CTAs an SM, whose 12 warps may have 168 registers a thread; a 14th would cost 40 of them, so
   // the producer writes the draft's K
@@ -42,7 +43,7 @@ struct TreeMma {
   static constexpr int kBarOff = kDescOff + kStages * 16;
   static constexpr int kScanOff = kBarOff + (2 * kStages + 6) * 8;
   static constexpr int kInfoOff = kScanOff + ((kThreads / 32 + 2) * 8 + 15) / 16 * 16;
-  using Split = TreeSplit<1, 7, 2>;
+  using Split = TreeSplit<7, 2>;
   using Info = TreePieceInfo<typename Split::Piece>;
   static_assert(kMlOff % 8 == 0 && kQOff % 16 == 0 && kDescOff % 16 == 0 && kBarOff % 8 == 0 && kScanOff % 8 == 0 &&
                     kInfoOff % alignof(Info) == 0,
@@ -53,13 +54,13 @@ struct TreeMma {
 
 // HERE: the CTAs join split groups themselves (tree_joins_here).  A form of its
 // own: the join's registers cost the page loop of long calls 5 to 9 %.
-template <int D, bool FP8, int WR, int WT, bool HERE>
-__global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 : 2) tree_mma_kernel(TreeLaunch a) {
-  using C = TreeMma<D, FP8, WR, WT>;
+template <int D, bool FP8, int WR, bool HERE>
+__global__ void __launch_bounds__(TreeMma<D, FP8, WR>::kThreads, WR > 1 ? 1 : 2) tree_mma_kernel(TreeLaunch a) {
+  using C = TreeMma<D, FP8, WR>;
   using Split = typename C::Split;
   using Info = typename C::Info;
   constexpr int P = 64, PB = C::kPageBytes, NST = C::kStages, NC = C::kConsumers, ND = C::kDraftWarps;
-  constexpr int KSTEPS = D / 16, NT = D / 8, CHUNKS = 4 / WT;
+  constexpr int KSTEPS = D / 16, NT = D / 8, WT = C::WT;
   constexpr uint32_t kAll = 0xffffffffu;
   constexpr DraftForm FORM = FP8 ? kDraftE4m3 : kDraftBf16;
   constexpr float kLift = FP8 ? kWeightLift : 0.f;
@@ -289,11 +290,9 @@ __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 
         vis[x] = row[x] >= rows ? 0 : all ? ~uint64_t(0) : draft ? anc[x] : tree_page_mask(pg, pc.hd, pos[x]);
       const uint32_t kst = smem_u32(stage + s * 2 * PB), vst = kst + PB;
       const uint8_t* kp8 = stage + s * 2 * PB;
-#pragma unroll
-      for (int c = 0; c < CHUNKS; ++c) {
-        const int tok0 = (wt * CHUNKS + c) * 16;
-        const uint32_t v0 = uint32_t(vis[0] >> tok0) & 0xffffu, v1 = uint32_t(vis[1] >> tok0) & 0xffffu;
-        if (!ok || !__any_sync(0xffffffffu, v0 | v1)) continue;
+      const int tok0 = wt * 16;
+      const uint32_t v0 = uint32_t(vis[0] >> tok0) & 0xffffu, v1 = uint32_t(vis[1] >> tok0) & 0xffffu;
+      if (ok && __any_sync(0xffffffffu, v0 | v1)) {
         float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
         if constexpr (FP8) {
 #pragma unroll
@@ -410,44 +409,42 @@ __global__ void __launch_bounds__(TreeMma<D, FP8, WR, WT>::kThreads, WR > 1 ? 1 
       l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
       m[x] -= kLift;  // what l and o are relative to
     }
-    if constexpr (WT > 1) {
-      if (wt > 0) {
+    if (wt > 0) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int at = (wt - 1) * C::kRows + row[x];
-          if (tq == 0) mlbuf[at * 2] = m[x], mlbuf[at * 2 + 1] = l[x];
+      for (int x = 0; x < 2; ++x) {
+        const int at = (wt - 1) * C::kRows + row[x];
+        if (tq == 0) mlbuf[at * 2] = m[x], mlbuf[at * 2 + 1] = l[x];
 #pragma unroll
-          for (int j = 0; j < NT; ++j)
-            *reinterpret_cast<float2*>(mbuf + at * C::kPitch + j * 8 + tq * 2) =
-                make_float2(o[j][2 * x], o[j][2 * x + 1]);
-        }
+        for (int j = 0; j < NT; ++j)
+          *reinterpret_cast<float2*>(mbuf + at * C::kPitch + j * 8 + tq * 2) =
+              make_float2(o[j][2 * x], o[j][2 * x + 1]);
       }
-      bar();
-      if (wt == 0) {
+    }
+    bar();
+    if (wt == 0) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float M = m[x], f[WT];
+      for (int x = 0; x < 2; ++x) {
+        float M = m[x], f[WT];
 #pragma unroll
-          for (int w = 1; w < WT; ++w) M = fmaxf(M, mlbuf[((w - 1) * C::kRows + row[x]) * 2]);
-          const float base = M == -INFINITY ? 0.f : M;
-          f[0] = fast_exp2(m[x] - base);
-          l[x] *= f[0];
+        for (int w = 1; w < WT; ++w) M = fmaxf(M, mlbuf[((w - 1) * C::kRows + row[x]) * 2]);
+        const float base = M == -INFINITY ? 0.f : M;
+        f[0] = fast_exp2(m[x] - base);
+        l[x] *= f[0];
+#pragma unroll
+        for (int w = 1; w < WT; ++w) {
+          const float* ml = mlbuf + ((w - 1) * C::kRows + row[x]) * 2;
+          f[w] = fast_exp2(ml[0] - base);
+          l[x] += f[w] * ml[1];
+        }
+        m[x] = M;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          o[j][2 * x] *= f[0], o[j][2 * x + 1] *= f[0];
 #pragma unroll
           for (int w = 1; w < WT; ++w) {
-            const float* ml = mlbuf + ((w - 1) * C::kRows + row[x]) * 2;
-            f[w] = fast_exp2(ml[0] - base);
-            l[x] += f[w] * ml[1];
-          }
-          m[x] = M;
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            o[j][2 * x] *= f[0], o[j][2 * x + 1] *= f[0];
-#pragma unroll
-            for (int w = 1; w < WT; ++w) {
-              const float2 v = *reinterpret_cast<const float2*>(
-                  mbuf + ((w - 1) * C::kRows + row[x]) * C::kPitch + j * 8 + tq * 2);
-              o[j][2 * x] += f[w] * v.x, o[j][2 * x + 1] += f[w] * v.y;
-            }
+            const float2 v = *reinterpret_cast<const float2*>(
+                mbuf + ((w - 1) * C::kRows + row[x]) * C::kPitch + j * 8 + tq * 2);
+            o[j][2 * x] += f[w] * v.x, o[j][2 * x + 1] += f[w] * v.y;
           }
         }
       }
@@ -516,7 +513,7 @@ __device__ __forceinline__ float dot4(float4 a, float4 b, float s) {
 
 template <int D, int P, bool HERE>
 __global__ void __launch_bounds__(kF32Threads) tree_f32_kernel(TreeLaunch a) {
-  using Split = TreeSplit<1, 4, 2>;
+  using Split = TreeSplit<4, 2>;
   using C = TreeF32<D, P>;
   constexpr int KP = C::kKPitch, VP = C::kVPitch;
   constexpr int SR = kF32Rows * P / kF32Threads;  // rows a thread scores (of one token)
@@ -698,10 +695,10 @@ __global__ void __launch_bounds__(kF32Threads) tree_f32_kernel(TreeLaunch a) {
 
 template <int D, bool FP8, int WR, bool HERE>
 cudaError_t launch_mma(const TreeLaunch& a, cudaStream_t s) {
-  using C = TreeMma<D, FP8, WR, 4>;
-  const cudaError_t e = allow_smem<tree_mma_kernel<D, FP8, WR, 4, HERE>>(C::kBytes);
+  using C = TreeMma<D, FP8, WR>;
+  const cudaError_t e = allow_smem<tree_mma_kernel<D, FP8, WR, HERE>>(C::kBytes);
   if (e != cudaSuccess) return e;
-  tree_mma_kernel<D, FP8, WR, 4, HERE><<<a.n_ctas, C::kThreads, C::kBytes, s>>>(a);
+  tree_mma_kernel<D, FP8, WR, HERE><<<a.n_ctas, C::kThreads, C::kBytes, s>>>(a);
   return cudaGetLastError();
 }
 

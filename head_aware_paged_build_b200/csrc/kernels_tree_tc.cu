@@ -80,7 +80,7 @@ struct TreeTc {
   static constexpr int kOffMl = kOffRaw + 2 * RS * kRaw;  // (m, l) of each row and stream
   static constexpr int kOffDesc = kOffMl + 2 * 128 * 8;
   static constexpr int kOffInfo = kOffDesc + kDescs * 8;
-  using Split = TreeSplit<1, 6, 8>;
+  using Split = TreeSplit<6, 8>;
   using Info = TreePieceInfo<typename Split::Piece>;
   static constexpr int kOffBar = kOffInfo + (2 * int(sizeof(Info)) + 7) / 8 * 8;
   static constexpr int kBytes = kOffBar + (22 + 2 * KS + 2 * VS + 4 * RS) * 8 + 8 + 8 * (RS > 0);

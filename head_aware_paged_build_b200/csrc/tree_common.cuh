@@ -8,9 +8,9 @@
 // and its ancestors, by the same rule at their positions.  A kv-head's rows
 // are its nodes times its group's q-heads, node-major.
 //
-// Split.  A head's work is its live pages, then the draft's page(s), in tiles
-// of `TP` pages, once for each row group, plus a fixed cost per group
-// (kStartTiles: loading Q, publishing or writing the rows).  Laid end to end
+// Split.  A head's work is its live pages, then the draft's page(s), once for
+// each row group, plus a fixed cost per group in pages (START: loading Q,
+// publishing or writing the rows).  Laid end to end
 // over the heads this is a line of U units; CTA c of G takes [cU/G, (c+1)U/G).
 // Every CTA works the line out from the table itself (a block-wide sum over
 // the heads), so the split follows the lengths as the cache grows and needs no
@@ -210,9 +210,8 @@ __device__ __forceinline__ void tree_draft_v(const TreeLaunch& a, const HeadDesc
   }
 }
 
-template <int TP, int START, int MIN_UNITS>
+template <int START, int MIN_UNITS>
 struct TreeSplit {
-  static constexpr int kStartTiles = START;  // fixed cost of a row group, in tiles
   int64_t units;                             // U
   int32_t ctas;                              // G, <= the grid
   int32_t head;                              // head the CTA's range starts in ...
@@ -232,7 +231,7 @@ struct TreeSplit {
     w.live = kind == 0 ? min(n_vpages, (ctx_len + a.P - 1) / a.P) : n_vpages;
     w.pages = w.live + (w.n + a.P - 1) / a.P;
     w.groups = (w.n + a.nodes_per_group - 1) / a.nodes_per_group;
-    w.per = (w.pages + TP - 1) / TP + START;
+    w.per = w.pages + START;
     return w;
   }
   __device__ __forceinline__ static int64_t head_units(const TreeLaunch& a, int h) {
@@ -347,8 +346,8 @@ struct TreeSplit {
       pc.node0 = group * a.nodes_per_group;
       pc.nodes = min(a.nodes_per_group, g.n - pc.node0);
       pc.live = g.live;
-      pc.p0 = int32_t(max(int64_t(0), x - START) * TP);
-      pc.p1 = int32_t(min(int64_t(g.pages), (y - START) * TP));
+      pc.p0 = int32_t(max(int64_t(0), x - START));
+      pc.p1 = int32_t(y - START);
       pc.first_cta = cta_of(at + START);
       pc.n_pieces = cta_of(at + g.per - 1) - pc.first_cta + 1;
       pc.first_slot = 2 * pc.first_cta + (cut(pc.first_cta) < at ? 1 : 0);
